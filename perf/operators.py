@@ -10,7 +10,7 @@ Four operators and the cache they share, a pool of fp32 states (slots, H, P, N):
   copy     ssd_cache_copy: pages of a pool copied, forked (one source, several
            destinations) and freed (zeroed), in every layer
   compact  ssd_cache_compact: live pages moved to the front of a pool with the
-           fewest moves, and the table of pages rewritten
+           fewest moves, and the table of pages that goes with it
 
 A case is a dict of plain values; "op" names the operator. Where `own` is false
 run() computes the plain forms below, in 32 bits, rounded once at the end.
@@ -290,8 +290,7 @@ def run(st):
             return y, st["after"]
         if op == "copy":
             return ssd.ssd_cache_copy(st["pool"], st["src"], st["dst"])
-        table = st["table"].clone()
-        live = ssd.ssd_cache_compact(st["pool"], table)
+        table, live = ssd.ssd_cache_compact(st["pool"], st["table"])
         return st["pool"], table, live
     return {"fwd": _plain_fwd, "step": _plain_step, "copy": _plain_copy, "compact": _plain_compact}[op](st)
 
