@@ -18,6 +18,11 @@ Functions carry the C names:
   ssd_segment_carry(fwd_states, fwd_decays, rev_states, rev_decays, seg) -> (fwd_in, rev_in)
   ssd_bidir_fwd_seeded(x, dt, A, B, C, D, fwd_init, rev_init)           -> out
   ssd_bidir_fwd_dtraw(x, dt_raw, dt_bias, A, B, C, D, dt_min, dt_max)   -> out
+Serving with the forward scan alone (causal.py):
+  ssd_causal_fwd(x, dt, A, B, C, D, init, seqlens=, slots=) -> (out, end states)
+  ssd_causal_step(x, dt, A, B, C, D, states, slots=)   -> out; the states advance in place
+  ssd_cache_copy(pool, src, dst)                       -> pool (pages copied, forked, cleared)
+  ssd_cache_compact(pool, table)                       -> (new table, number of live pages)
 The sequence-sharded mixer over a process group is in seqshard.py; the
 block-diffusion cache of several layers and the CUDA-graph block loop are in
 blockdiff.py.
@@ -28,6 +33,7 @@ Shapes (row-major, natural token order; [0] forward, [1] reverse):
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -35,13 +41,15 @@ from . import _lib as _c
 from ._lib import (SSD_PATH_AUTO, SSD_PATH_SIMT, SSD_PATH_CHUNKED, SSD_PATH_FUSED, SSD_PATH_SEGMENTED,  # noqa: F401
                    SSD_PATH_PAIR, SSD_PATH_BLOCK, SSD_PATH_ONETILE,
                    SSD_OK, SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_CUDA,
-                   SSD_ERR_WORKSPACE, SSD_ERR_TIMEOUT, SSD_OP_BIDIR_FWD, SSD_OP_PREFIX_STATE,
-                   SSD_OP_BLOCK_STEP, SSD_OP_BIDIR_BWD, SSD_OP_BIDIR_FWD_X2, SSD_OP_MIXER_BLOCK)
+                   SSD_ERR_WORKSPACE, SSD_ERR_TIMEOUT, SSD_ERR_INDEX, SSD_OP_BIDIR_FWD, SSD_OP_PREFIX_STATE,
+                   SSD_OP_BLOCK_STEP, SSD_OP_BIDIR_BWD, SSD_OP_BIDIR_FWD_X2, SSD_OP_MIXER_BLOCK,
+                   SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP)
 
 __all__ = ["ssd_bidir_fwd", "ssd_bidir_bwd", "ssd_bidir_fwd_x2", "ssd_mixer_block_fwd", "ssd_prefix_state",
            "ssd_prefix_state_layers", "ssd_block_step",
            "ssd_segment_states",
-           "ssd_segment_carry", "ssd_bidir_fwd_seeded", "ssd_bidir_fwd_dtraw", "ssd_workspace_bytes",
+           "ssd_segment_carry", "ssd_bidir_fwd_seeded", "ssd_bidir_fwd_dtraw",
+           "ssd_causal_fwd", "ssd_causal_step", "ssd_cache_copy", "ssd_cache_compact", "ssd_workspace_bytes",
            "ssd_get_device_status", "SSDError", "Workspace", "lib"]
 
 lib = _c.load()
@@ -99,6 +107,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.buf = None
+        self.lock = threading.Lock()   # held by calls that make several launches on the buffer
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
@@ -536,3 +545,6 @@ def ssd_mixer_block_fwd(xbc, z, dt_raw, conv_w, conv_b, dt_bias, A, D, norm_w, n
                                  ctypes.c_void_p(stream))
     _check(rc, "ssd_mixer_block_fwd")
     return out
+
+
+from .causal import ssd_cache_compact, ssd_cache_copy, ssd_causal_fwd, ssd_causal_step  # noqa: E402

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "ssd_bidir.h"
+#include "ssd_causal.h"
 #include "ssd_kernels.h"
 
 using ssd::SimtArgs;
@@ -174,6 +175,8 @@ extern "C" {
 
 size_t ssd_workspace_bytes(int op, int batch, int seqlen, int nheads, int headdim, int dstate,
                            int ngroups, int chunk, int dtype) {
+    if (op == SSD_OP_CAUSAL_FWD || op == SSD_OP_CAUSAL_STEP)
+        return ssd::causal_workspace_bytes(op, batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
     const bool use_chunk = op != SSD_OP_BLOCK_STEP;
     if (check_shape(batch, seqlen, nheads, headdim, dstate, ngroups, chunk, dtype, use_chunk) != SSD_OK)
         return 0;
@@ -643,7 +646,8 @@ int ssd_get_device_status(const void *workspace, void *stream) {
     if (cudaMemcpy(&st, workspace, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return SSD_ERR_CUDA;
     if (st.flags == 0) return SSD_OK;
     if (cudaMemset(const_cast<void *>(workspace), 0, sizeof(st)) != cudaSuccess) return SSD_ERR_CUDA;
-    return (st.flags & ssd::kFlagTimeout) ? SSD_ERR_TIMEOUT : SSD_ERR_CUDA;
+    if (st.flags & ssd::kFlagTimeout) return SSD_ERR_TIMEOUT;
+    return (st.flags & ssd::kFlagIndex) ? SSD_ERR_INDEX : SSD_ERR_CUDA;
 }
 
 const char *ssd_error_string(int status) {
@@ -654,6 +658,7 @@ const char *ssd_error_string(int status) {
         case SSD_ERR_CUDA: return "CUDA launch or runtime error";
         case SSD_ERR_WORKSPACE: return "workspace missing or too small";
         case SSD_ERR_TIMEOUT: return "a bounded device-side wait expired";
+        case SSD_ERR_INDEX: return "a slot or page index was out of range or named twice";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,311 @@
+// The causal scan over prompts on CUDA cores, in fp32 whatever the I/O type,
+// token by token:
+//   H <- exp(dt_t A_h) H + dt_t x_t B_t^T,   y_t = H C_t + D x_t
+// and the pieces that every path of the prompts shares: the resolving of pool
+// slots and the carry of states across segments.
+//
+// The state's columns p do not depend on one another, so a CTA takes COLS of a
+// head's P columns and walks its tokens with that part of the state in
+// registers: a thread owns 4 p x 8 n, reads 16 operands a token from shared
+// memory for its 96 operations (packed two to an instruction, f32x2) and meets
+// the other n in a butterfly. Tokens arrive in chunks of kTok through
+// cp.async, two chunks deep. What bounds it: instruction issue (about 75 a
+// token and warp) with many units, the token chain's latency with few; there
+// the sequence is cut into segments (own end states, a carry, then the
+// outputs), which costs a second pass over x and B.
+#include <stdint.h>
+
+#include "ssd_causal.h"
+#include "ssd_kernels.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kTok = 16;
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// four consecutive elements of shared memory
+__device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 lds4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+
+template <typename T, int N, int COLS>
+struct SimtSmem {
+    T B[2][kTok][N], C[2][kTok][N], x[2][kTok][COLS];
+    float2 gd[2][kTok];   // decay and step size of a token
+};
+
+template <typename T, int N, int COLS, int MODE>
+__global__ void __launch_bounds__(COLS *N / 32)
+causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
+    constexpr int THREADS = COLS * N / 32;
+    constexpr int NG = N / 8;                 // lanes that share a column
+    constexpr bool OUT = MODE == kCausalOutput;
+    using S = SimtSmem<T, N, COLS>;
+    extern __shared__ __align__(16) uint8_t raw[];
+    S &sm = *reinterpret_cast<S *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gn = lane % NG, cg = (warp * 32 + lane) / NG;   // n group, column group (4 columns)
+    const int parts = a.P / COLS;
+    const int part = blockIdx.x % parts;
+    const int seg = (blockIdx.x / parts) % sg.count;
+    const int bh = blockIdx.x / parts / sg.count;
+    const int b = bh / a.H, h = bh % a.H;
+    const int len = a.len(b), first = seg * sg.tokens;
+    const int stop = sg.count == 1 ? a.L : min(a.L, first + sg.tokens);   // rows of this segment
+    const int end = max(first, min(len, stop));                           // the ones that hold tokens
+    const int row = a.rows ? a.rows[b] : b;
+    T *out = static_cast<T *>(a.out) + ((size_t)b * a.L * a.H + h) * a.P + part * COLS;   // + t H P
+    // zero rows [t, stop): behind the sequence, or the whole row of a skipped one
+    auto blank = [&](int t) {
+        const int chunks = COLS * (int)sizeof(T) / 16;
+        for (int i = t * chunks + tid; i < stop * chunks; i += THREADS)
+            reinterpret_cast<uint4 *>(out + (size_t)(i / chunks) * a.H * a.P)[i % chunks] = make_uint4(0, 0, 0, 0);
+    };
+    if (row < 0) {
+        if (OUT) blank(first);
+        return;
+    }
+    if (!OUT && first + sg.tokens >= len) return;   // no segment behind this one reads its state
+    const T *xp = static_cast<const T *>(a.x) + (long long)b * a.x_sb + (size_t)h * a.P + part * COLS;
+    const int g = h / (a.H / a.G);
+    const T *Bp = static_cast<const T *>(a.B) + (long long)b * a.b_sb + (size_t)g * N;
+    const T *Cp = static_cast<const T *>(a.C) + (long long)b * a.c_sb + (size_t)g * N;
+    const T *dtp = static_cast<const T *>(a.dt) + (long long)b * a.dt_sb + h;
+    const float A = a.A[h], D = OUT && a.D ? a.D[h] : 0.f;
+
+    // state: element (4 cg + k, n) with n = 4 gn + i (i < 4) and N / 2 + 4 gn + i
+    f32x2 H[4][4];
+    const size_t col = (size_t)part * COLS + 4 * cg;
+    const float *start = nullptr;
+    if (OUT && sg.count > 1) start = sg.state + (((size_t)bh * sg.count + seg) * a.P + col) * N;
+    else if (OUT && a.init) start = a.init + (((size_t)row * a.H + h) * a.P + col) * N;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (start) v = *reinterpret_cast<const float4 *>(start + (size_t)k * N + q * (N / 2) + 4 * gn);
+            H[k][2 * q] = pack2(v.x, v.y);
+            H[k][2 * q + 1] = pack2(v.z, v.w);
+        }
+
+    float raw_dt = 0.f;
+    auto fetch = [&](int t0, int buf) {
+        const int m = min(kTok, end - t0);
+        constexpr int EPC = 16 / (int)sizeof(T);
+        for (int i = tid; i < m * (N / EPC); i += THREADS) {
+            const int t = i / (N / EPC), c = (i % (N / EPC)) * EPC;
+            cp_async16(&sm.B[buf][t][c], Bp + (long long)(t0 + t) * a.b_st + c);
+            if (OUT) cp_async16(&sm.C[buf][t][c], Cp + (long long)(t0 + t) * a.c_st + c);
+        }
+        for (int i = tid; i < m * (COLS / EPC); i += THREADS) {
+            const int t = i / (COLS / EPC), c = (i % (COLS / EPC)) * EPC;
+            cp_async16(&sm.x[buf][t][c], xp + (long long)(t0 + t) * a.x_st + c);
+        }
+        cp_commit();
+        if (tid < m) raw_dt = IO<T>::load(dtp + (long long)(t0 + tid) * a.dt_st);
+    };
+    float sum = 0.f;          // sum of the step sizes (thread t < kTok: its tokens' share)
+    int buf = 0;
+    if (first < end) fetch(first, 0);
+    for (int t0 = first; t0 < end; t0 += kTok, buf ^= 1) {
+        const int m = min(kTok, end - t0);
+        if (tid < m) {
+            const float v = a.step(raw_dt, h);
+            sm.gd[buf][tid] = make_float2(expf(v * A), v);
+            sum += v;
+        }
+        cp_wait();
+        __syncthreads();      // chunk here; the other buffer is read by nobody
+        if (t0 + kTok < end) fetch(t0 + kTok, buf ^ 1);
+#pragma unroll 2
+        for (int t = 0; t < m; ++t) {
+            const float2 gd = sm.gd[buf][t];
+            const float4 x = lds4(&sm.x[buf][t][4 * cg]);
+            const float4 b0 = lds4(&sm.B[buf][t][4 * gn]), b1 = lds4(&sm.B[buf][t][N / 2 + 4 * gn]);
+            const f32x2 Bv[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
+            const f32x2 G = pack2(gd.x, gd.x);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float u = gd.y * xs[k];
+                const f32x2 U = pack2(u, u);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) H[k][q] = fma2(H[k][q], G, mul2(U, Bv[q]));
+            }
+            if (OUT) {
+                const float4 c0 = lds4(&sm.C[buf][t][4 * gn]), c1 = lds4(&sm.C[buf][t][N / 2 + 4 * gn]);
+                const f32x2 Cv[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 s = fma2(H[k][3], Cv[3], fma2(H[k][2], Cv[2], fma2(H[k][1], Cv[1], mul2(H[k][0], Cv[0]))));
+                    const float2 f = unpack2(s);
+                    y[k] = f.x + f.y;
+                }
+                // butterfly over the NG lanes of a column group: two steps halve the
+                // columns a lane carries, the others add
+                const bool u1 = gn & (NG / 2), u2 = gn & (NG / 4);
+                const float r0 = (u1 ? y[2] : y[0]) + __shfl_xor_sync(0xffffffffu, u1 ? y[0] : y[2], NG / 2);
+                const float r1 = (u1 ? y[3] : y[1]) + __shfl_xor_sync(0xffffffffu, u1 ? y[1] : y[3], NG / 2);
+                float r = (u2 ? r1 : r0) + __shfl_xor_sync(0xffffffffu, u2 ? r0 : r1, NG / 4);
+#pragma unroll
+                for (int o = NG / 8; o >= 1; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+                if ((gn & (NG / 4 - 1)) == 0) {
+                    const int k = (u1 ? 2 : 0) + (u2 ? 1 : 0);
+                    const float xk = u1 ? (u2 ? x.w : x.z) : (u2 ? x.y : x.x);
+                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + 4 * cg + k, a.D ? fmaf(D, xk, r) : r);
+                }
+            }
+        }
+    }
+    if (OUT) blank(end);
+    // the state behind the last token: the sequence's own, or the segment's
+    float *last = nullptr;
+    if (!OUT) {
+        last = sg.state + (((size_t)bh * sg.count + seg) * a.P + col) * N;
+        // decay over the segment: thread t holds the step sizes of tokens t mod kTok
+        if (warp == 0) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0 && part == 0) sg.decay[(size_t)bh * sg.count + seg] = expf(sum * A);
+        }
+    } else if (a.state_out && (sg.count == 1 || (end > first && end == len) || (len == 0 && seg == 0))) {
+        last = a.state_out + (((size_t)row * a.H + h) * a.P + col) * N;
+    }
+    if (last) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float2 u = unpack2(H[k][2 * q]), v = unpack2(H[k][2 * q + 1]);
+                *reinterpret_cast<float4 *>(last + (size_t)k * N + q * (N / 2) + 4 * gn) = make_float4(u.x, u.y, v.x, v.y);
+            }
+    }
+}
+
+// One CTA per row: a row is padding (-1), out of range, named by an earlier
+// row, or its own slot.
+__global__ void __launch_bounds__(128) resolve_slots_kernel(const int *slots, int nslots, int *rows, DeviceStatus *st) {
+    const int b = blockIdx.x, s = slots[b];
+    bool bad = s < -1 || s >= nslots;
+    bool again = false;
+    if (s >= 0)
+        for (int i = threadIdx.x; i < b; i += 128) again |= slots[i] == s;
+    bad |= (bool)__syncthreads_or(again);
+    if (threadIdx.x == 0) {
+        rows[b] = bad ? -1 : s;
+        if (bad) atomicOr(&st->flags, kFlagIndex);
+    }
+}
+
+// Own end states of the segments -> the states entering them, in place: thread
+// by thread over a state's elements, in the order of the segments.
+__global__ void __launch_bounds__(256) causal_carry_kernel(const CausalArgs a, const CausalSegments sg) {
+    const int per = a.P * a.N / 4;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (long long)a.batch * a.H * per) return;
+    const long long bh = i / per;
+    const int e = (int)(i % per);
+    const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+    const int row = a.rows ? a.rows[b] : b;
+    if (row < 0) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.init) s = reinterpret_cast<const float4 *>(a.init)[((size_t)row * a.H + h) * per + e];
+    float4 *st = reinterpret_cast<float4 *>(sg.state) + bh * sg.count * per + e;
+    const float *dc = sg.decay + bh * sg.count;
+    // segments that start behind the sequence are never read
+    const int n = min(sg.count, (a.len(b) + sg.tokens - 1) / sg.tokens);
+    for (int g = 0; g < (n < 1 ? 1 : n); ++g) {
+        const float4 own = g + 1 < n ? st[(size_t)g * per] : s;
+        st[(size_t)g * per] = s;
+        if (g + 1 < n) {
+            const float d = dc[g];
+            s = make_float4(fmaf(d, s.x, own.x), fmaf(d, s.y, own.y), fmaf(d, s.z, own.z), fmaf(d, s.w, own.w));
+        }
+    }
+}
+
+constexpr int kCols = 16;   // columns of a CTA
+
+template <typename T, int N>
+cudaError_t run_simt(const CausalArgs &a, const CausalSegments &s, int mode, cudaStream_t stream) {
+    const long long grid = (long long)a.batch * a.H * s.count * (a.P / kCols);
+    if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
+    const int threads = kCols * N / 32;
+    const size_t smem = sizeof(SimtSmem<T, N, kCols>);
+    static_assert(sizeof(SimtSmem<T, N, kCols>) <= 48 * 1024, "shared memory within the default limit");
+    if (mode == kCausalOutput) causal_simt_kernel<T, N, kCols, kCausalOutput><<<(unsigned)grid, threads, smem, stream>>>(a, s);
+    else causal_simt_kernel<T, N, kCols, kCausalState><<<(unsigned)grid, threads, smem, stream>>>(a, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_resolve_slots(const int *slots, int batch, int nslots, int *rows, DeviceStatus *st,
+                                 cudaStream_t stream) {
+    resolve_slots_kernel<<<batch, 128, 0, stream>>>(slots, nslots, rows, st);
+    return cudaGetLastError();
+}
+
+// Segments of at least 128 tokens, as many as it takes to give every SM 16
+// warps of work.
+void causal_simt_segments(int batch, int L, int H, int P, int N, int sms, int *count, int *tokens) {
+    const long long ctas = (long long)batch * H * (P / kCols);
+    const long long want = 16LL * sms / (kCols * N / 1024);
+    long long n = ctas > 0 ? want / ctas : 1;
+    const long long most = L / 128;
+    n = n < most ? n : most;
+    if (n < 2) {
+        *count = 1;
+        *tokens = L;
+        return;
+    }
+    *tokens = (int)((L + n - 1) / n);
+    *count = (L + *tokens - 1) / *tokens;
+}
+
+cudaError_t launch_causal_simt(const CausalArgs &a, const CausalSegments &s, int mode, cudaStream_t stream) {
+    if (a.bf16) return a.N == 128 ? run_simt<__nv_bfloat16, 128>(a, s, mode, stream) : run_simt<__nv_bfloat16, 64>(a, s, mode, stream);
+    return a.N == 128 ? run_simt<float, 128>(a, s, mode, stream) : run_simt<float, 64>(a, s, mode, stream);
+}
+
+cudaError_t launch_causal_carry(const CausalArgs &a, const CausalSegments &s, cudaStream_t stream) {
+    const long long threads = (long long)a.batch * a.H * a.P * a.N / 4;
+    causal_carry_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(a, s);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

@@ -18,7 +18,7 @@ struct DeviceStatus {
     unsigned int pad[61];
 };
 static_assert(sizeof(DeviceStatus) == kStatusBytes, "status header size");
-enum : unsigned int { kFlagTimeout = 1u };
+enum : unsigned int { kFlagTimeout = 1u, kFlagIndex = 2u };
 
 __device__ __forceinline__ void report_timeout(DeviceStatus *st, unsigned int where) {
     if (st) {

@@ -73,13 +73,15 @@ enum {
     SSD_ERR_UNSUPPORTED = -2,   /* valid but not implemented: headdim, dstate, chunk, dtype */
     SSD_ERR_CUDA = -3,          /* a CUDA launch or driver call failed (cudaGetLastError) */
     SSD_ERR_WORKSPACE = -4,     /* workspace NULL or smaller than ssd_workspace_bytes() */
-    SSD_ERR_TIMEOUT = -5        /* a bounded device-side wait expired (from ssd_get_device_status) */
+    SSD_ERR_TIMEOUT = -5,       /* a bounded device-side wait expired (from ssd_get_device_status) */
+    SSD_ERR_INDEX = -6          /* a slot or page index in device memory was out of range, or a slot was
+                                   named twice in one call (from ssd_get_device_status) */
 };
 
 /* Operation ids for ssd_workspace_bytes. */
 enum {
     SSD_OP_BIDIR_FWD = 0, SSD_OP_PREFIX_STATE = 1, SSD_OP_BLOCK_STEP = 2, SSD_OP_BIDIR_BWD = 3,
-    SSD_OP_BIDIR_FWD_X2 = 4, SSD_OP_MIXER_BLOCK = 5
+    SSD_OP_BIDIR_FWD_X2 = 4, SSD_OP_MIXER_BLOCK = 5, SSD_OP_CAUSAL_FWD = 6, SSD_OP_CAUSAL_STEP = 7
 };
 
 /* Kernel selection for ssd_bidir_fwd_path (tests and benchmarks). */
@@ -386,6 +388,92 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
                          int batch, int seqlen, int nheads, int headdim, int dstate, int ngroups,
                          int dtype, void *workspace, size_t ws_bytes, void *stream);
 
+/* Serving with the forward scan alone. The forward state of a prefix is a
+ * cache that decoding reuses exactly ("Training Hybrid Block Diffusion
+ * Language Models with Partial Bidirectionality", Abstract: prefix-only states
+ * reused exactly); the four calls below fill such a cache from prompts with
+ * the prompts' outputs, advance it by single tokens, and move its pages.
+ *
+ * Differences from the conventions above, for these four calls only:
+ *  - headdim is a multiple of 64 up to 256.
+ *  - x, B, C and dt may be strided in batch and token, e.g. views of one
+ *    projection: (nheads, headdim) and (ngroups, dstate) are contiguous and
+ *    the strides, in elements, are at least one such row; x, B and C strides
+ *    are multiples of 16 bytes. Strides of dimensions of size 1 are ignored.
+ *    dt needs only its element's alignment.
+ *  - States live in a pool (nslots, nheads, headdim, dstate) fp32 and `slots`
+ *    (batch) int32 in device memory gives each row's page. Slot -1 is a padding
+ *    row: its output is zero and no state is read or written. A slot outside
+ *    [-1, nslots), or one that an earlier row of the call names, is treated as
+ *    -1 and reported as SSD_ERR_INDEX by ssd_get_device_status. With slots NULL
+ *    the pool has one page a row, in order, and nslots is ignored.
+ *  - init_state / state and state_out are the same array (in place) or do not
+ *    overlap. Pages that no row names are left as they were.
+ *  - dt_bias NULL: dt is the step size. Otherwise it is the raw projection and
+ *    the step size min(max(softplus(dt + dt_bias[h]), dt_min), dt_max), as for
+ *    ssd_bidir_fwd_dtraw, kept in fp32. D may be NULL (no skip term).
+ *  - Forward only: there is no backward pass of these calls. */
+
+/* Prompts: from the start state (page of init_state, or zero where it is NULL),
+ *   h_t = exp(dt_t A_h) h_{t-1} + dt_t B_t x_t^T,   out_t = C_t^T h_t + D_h x_t
+ * and the state after each sequence's last token.
+ *   x        (batch, seqlen, nheads, headdim)      io
+ *   dt       (batch, seqlen, nheads)               io
+ *   A, D, dt_bias (nheads)                         fp32; D, dt_bias nullable
+ *   B, C     (batch, seqlen, ngroups, dstate)      io
+ *   seqlens  (batch) int32 in device memory, or NULL (every sequence has seqlen
+ *            tokens); values are clamped to [0, seqlen]. Rows behind a
+ *            sequence's end are not read as values (they may hold anything, NaN
+ *            included) and their outputs are zero. A sequence of no tokens
+ *            leaves its start state as its end state.
+ *   out      (batch, seqlen, nheads, headdim)      io, contiguous, overwritten
+ *   state_out pool fp32, nullable (the end states are not wanted)
+ * Within a sequence a non-finite input makes the outputs of its own tile of 128
+ * tokens undefined, not only those behind it.
+ * path: SSD_PATH_AUTO or SSD_PATH_SIMT (the CUDA-core scan). Workspace:
+ * ssd_workspace_bytes with SSD_OP_CAUSAL_FWD (chunk is ignored). */
+int ssd_causal_fwd(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                   const float *dt_bias, float dt_min, float dt_max, const int *seqlens, const int *slots,
+                   const float *init_state, float *state_out, void *out, long long x_batch, long long x_token,
+                   long long dt_batch, long long dt_token, long long B_batch, long long B_token, long long C_batch,
+                   long long C_token, int nslots, int batch, int seqlen, int nheads, int headdim, int dstate,
+                   int ngroups, int dtype, int path, void *workspace, size_t ws_bytes, void *stream);
+
+/* Single tokens: the same recurrence for one token of each row.
+ *   x (batch, nheads, headdim), dt (batch, nheads), B, C (batch, ngroups, dstate)  io
+ *   state, state_out  pools fp32 (state_out == state: in place)
+ *   out (batch, nheads, headdim)  io, contiguous, overwritten
+ * One launch (two past 2048 rows with slots). Workspace
+ * (ssd_workspace_bytes with SSD_OP_CAUSAL_STEP) only with slots; else NULL. */
+int ssd_causal_step(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                    const float *dt_bias, float dt_min, float dt_max, const int *slots, const float *state,
+                    float *state_out, void *out, long long x_batch, long long dt_batch, long long B_batch,
+                    long long C_batch, int nslots, int batch, int nheads, int headdim, int dstate, int ngroups,
+                    int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* Pages of a pool (layers, nslots, page_bytes) of any element type: for i = 0 ..
+ * n - 1, in this order and in every layer, page dst[i] <- page src[i], or zero
+ * where src[i] is -1 (a freed page). One source with several destinations
+ * forks it; the order also defines chains and repeated destinations. dst[i] =
+ * -1 leaves the pair out; so does an index outside [-1, nslots), reported as
+ * SSD_ERR_INDEX. src, dst (n) int32 in device memory. nslots <= 524288.
+ * Workspace: the 256-byte status header. */
+int ssd_cache_copy(void *pool, long long page_bytes, int layers, int nslots, const int *src, const int *dst, int n,
+                   void *workspace, size_t ws_bytes, void *stream);
+
+/* Compaction of such a pool: the pages that `table` (rows, int32, -1 for none;
+ * several rows may share a page) names move to the front with the fewest
+ * moves. With n distinct pages named, pages below n stay and the k-th named
+ * page from n on moves to the k-th page below n that no row names.
+ *   table_out (rows)  the table that goes with the moved pages; must not
+ *                     overlap table. Indices outside [-1, nslots) become -1 and
+ *                     are reported as SSD_ERR_INDEX.
+ *   live_out  (1)     n
+ * Pages from n on keep their bytes and are free. Workspace: the 256-byte status
+ * header. */
+int ssd_cache_compact(void *pool, long long page_bytes, int layers, int nslots, const int *table, int rows,
+                      int *table_out, int *live_out, void *workspace, size_t ws_bytes, void *stream);
+
 /* ssd_bidir_fwd for callers that cannot allocate device memory when they
  * call the mixer: code running under CUDA graph capture in the global mode,
  * where cudaMalloc is not allowed; plug-ins inside a runtime that has already
@@ -424,7 +512,8 @@ int ssd_noalloc_get_status(void *stream);
 
 /* Synchronise `stream`, read and clear the workspace's status header.
  * Returns SSD_OK, SSD_ERR_TIMEOUT (a bounded device wait expired in a call
- * since the last check) or SSD_ERR_CUDA (the stream reported an error). */
+ * since the last check), SSD_ERR_INDEX (a call since the last check met a bad
+ * slot or page index) or SSD_ERR_CUDA (the stream reported an error). */
 int ssd_get_device_status(const void *workspace, void *stream);
 
 /* Self-test of the bounded device waits: launches one CTA that waits on an
