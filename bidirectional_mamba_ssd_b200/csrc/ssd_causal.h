@@ -70,6 +70,11 @@ cudaError_t launch_causal_simt(const CausalArgs &a, const CausalSegments &s, int
 // Own end states -> states entering every segment (the start state included).
 cudaError_t launch_causal_carry(const CausalArgs &a, const CausalSegments &s, cudaStream_t stream);
 
+// Tensor-core scan (ssd_causal_tc.cu), bf16 I/O, L >= 1: resolves slots and lengths
+// by itself; `scratch` is behind the workspace's status header.
+size_t causal_tc_scratch_bytes(int batch, int N);
+cudaError_t launch_causal_tc(const CausalArgs &a, void *scratch, cudaStream_t stream);
+
 cudaError_t launch_causal_step(const CausalArgs &a, cudaStream_t stream);
 
 // ssd_workspace_bytes of the causal operators (0: sizes they reject).

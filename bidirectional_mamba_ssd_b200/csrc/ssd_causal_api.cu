@@ -46,14 +46,13 @@ int sm_count() {
     return n > 0 ? n : 148;
 }
 
-// Workspace of ssd_causal_fwd: status header, resolved rows, segment states.
+// Workspace of the CUDA-core scan: status header, resolved rows, segment states.
 struct Plan {
     CausalSegments seg;
     size_t rows, state, decay, total;
 };
-Plan plan(int path, int batch, int seqlen, int nheads, int headdim, int dstate) {
+Plan plan(int batch, int seqlen, int nheads, int headdim, int dstate) {
     Plan p{};
-    (void)path;
     ssd::causal_simt_segments(batch, seqlen, nheads, headdim, dstate, sm_count(), &p.seg.count, &p.seg.tokens);
     size_t o = ssd::kStatusBytes;
     p.rows = o;
@@ -69,9 +68,16 @@ Plan plan(int path, int batch, int seqlen, int nheads, int headdim, int dstate) 
     return p;
 }
 
-int causal_path(int path, int dtype) {
-    (void)dtype;
-    return path == SSD_PATH_AUTO ? SSD_PATH_SIMT : path;
+// SSD_PATH_AUTO: bf16 on the tensor cores, fp32 (and an empty sequence, whose end
+// state is its start state) on the CUDA cores.
+int causal_path(int path, int seqlen, int dtype) {
+    if (path == SSD_PATH_AUTO) path = dtype == SSD_BF16 ? SSD_PATH_FUSED : SSD_PATH_SIMT;
+    return seqlen == 0 ? SSD_PATH_SIMT : path;
+}
+
+size_t fwd_bytes(int path, int batch, int seqlen, int nheads, int headdim, int dstate) {
+    return path == SSD_PATH_FUSED ? ssd::kStatusBytes + ssd::causal_tc_scratch_bytes(batch, dstate)
+                                  : plan(batch, seqlen, nheads, headdim, dstate).total;
 }
 
 // Rows from which the single-token kernel's CTAs no longer look for repeated
@@ -84,7 +90,10 @@ namespace ssd {
 size_t causal_workspace_bytes(int op, int batch, int seqlen, int nheads, int headdim, int dstate, int ngroups, int dtype) {
     if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
     if (op == SSD_OP_CAUSAL_STEP) return kStatusBytes + (batch > kScanRows ? round256(sizeof(int) * (size_t)batch) : 0);
-    return plan(SSD_PATH_SIMT, batch, seqlen, nheads, headdim, dstate).total;
+    // whichever path is asked for
+    const size_t s = fwd_bytes(SSD_PATH_SIMT, batch, seqlen, nheads, headdim, dstate);
+    const size_t t = dtype == SSD_BF16 ? fwd_bytes(SSD_PATH_FUSED, batch, seqlen, nheads, headdim, dstate) : 0;
+    return s > t ? s : t;
 }
 }  // namespace ssd
 
@@ -98,12 +107,12 @@ int ssd_causal_fwd(const void *x, const void *dt, const float *A, const void *B,
                    int ngroups, int dtype, int path, void *workspace, size_t ws_bytes, void *stream) {
     const int rc = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
     if (rc != SSD_OK) return rc;
-    if (path != SSD_PATH_AUTO && path != SSD_PATH_SIMT) return SSD_ERR_INVALID_ARG;
+    if (path != SSD_PATH_AUTO && path != SSD_PATH_SIMT && path != SSD_PATH_FUSED) return SSD_ERR_INVALID_ARG;
+    if (path == SSD_PATH_FUSED && dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     if (!workspace) return SSD_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SSD_ERR_INVALID_ARG;
-    path = causal_path(path, dtype);
-    const Plan p = plan(path, batch, seqlen, nheads, headdim, dstate);
-    if (ws_bytes < p.total) return SSD_ERR_WORKSPACE;
+    path = causal_path(path, seqlen, dtype);
+    if (ws_bytes < fwd_bytes(path, batch, seqlen, nheads, headdim, dstate)) return SSD_ERR_WORKSPACE;
     if (dt_bias && (!(dt_min >= 0.f) || !(dt_max >= dt_min))) return SSD_ERR_INVALID_ARG;
     if (slots && nslots < 0) return SSD_ERR_INVALID_ARG;
     if (batch == 0) return SSD_OK;
@@ -136,6 +145,8 @@ int ssd_causal_fwd(const void *x, const void *dt, const float *A, const void *B,
     a.status = reinterpret_cast<ssd::DeviceStatus *>(ws);
     a.batch = batch; a.L = seqlen; a.H = nheads; a.P = headdim; a.G = ngroups; a.N = dstate;
     a.bf16 = dtype == SSD_BF16;
+    if (path == SSD_PATH_FUSED) return to_status(ssd::launch_causal_tc(a, ws + ssd::kStatusBytes, s));
+    const Plan p = plan(batch, seqlen, nheads, headdim, dstate);
     if (slots) {
         int *rows = reinterpret_cast<int *>(ws + p.rows);
         const cudaError_t err = ssd::launch_resolve_slots(slots, batch, nslots, rows, a.status, s);

@@ -1,0 +1,975 @@
+// The causal scan over prompts on the tensor cores (bf16 I/O), one persistent
+// CTA per SM.
+//
+// Mathematics, per (batch row, 64 columns of a head) = unit and tile of 128
+// tokens, with a_t = A * (dt_1 + .. + dt_t) inside the tile and H the state
+// entering it:
+//   y_t = sum_{s <= t} (C_t . B_s) exp(a_t - a_s) dt_s x_s + exp(a_t) C_t H + D x_t
+//   H  <- exp(a_T) H + sum_s exp(a_T - a_s) dt_s B_s x_s^T
+// Four products a tile: G = C B^T, Y = M X with M = G c_s under the causal mask,
+// Yo = C H, S = B^T diag(w) X.
+//
+// The decay between two tokens is split at the tile's half decay a_r = a_T / 2:
+//   exp(a_t - a_s) = exp(a_t - a_r) * exp(a_r - a_s)
+// so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, and the row's
+// factor is applied to the fp32 output. Both stay within e^+-60 while the tile's
+// decay is at most 120; past that (a test on the tile) each entry takes its own
+// exponential.
+//
+// Roundings to bf16: M and the copy of H that enters C H, both operands of
+// products whose result is rounded to bf16 (relative 2^-9 a term, random). The
+// state is a result in fp32, so diag(w) X enters S as two bf16 terms, the rounded
+// product and its remainder (relative 2^-18 a term), and H stays in fp32 registers.
+//
+// What bounds it: HBM (x, B, C and y once). Work is cut so that every CTA has
+// the same number of tiles: the tiles of all units in order, divided evenly. A
+// unit that a cut falls into is shared by two neighbouring CTAs. With a unit or
+// more per CTA the first part of a shared unit is its CTA's first work and the
+// second part its CTA's last, so the state crosses through global memory long
+// before it is wanted. With fewer units (long sequences) a pass over x and B gives
+// every part's own end state, a small kernel chains them, and the outputs follow.
+//
+// Roles (448 threads): warp 0 TMA producer; warp 1 MMA issuer, which polls what
+// is ready (S, then Y and Yo, then G) instead of waiting in a fixed order; warps
+// 2..5 group C: decays, diag(w) X, the state; warps 6..9 and 10..13 groups A and B:
+// mask and output of the even and the odd tiles, so that one tile's mask overlaps
+// the other's products and output. In a group, thread r owns tile row r.
+// TMEM (512 columns): two of {G 128: M packed over its first half once read, Yo over
+// its second}, two Y, two S. Shared memory: C and B two tiles deep, x two, H and
+// the two terms of diag(w) X once.
+// Every wait is bounded; one that expires sets the workspace's timeout flag and
+// the CTA runs to its end without storing.
+#include <cuda.h>
+#include <stdint.h>
+
+#include "sm100.cuh"
+#include "ssd_causal.h"
+#include "ssd_fused_util.cuh"
+#include "ssd_kernels.h"
+#include "ssd_tmap.h"
+
+namespace ssd {
+namespace {
+
+using namespace sm100;
+using namespace fused;
+
+constexpr int kTile = 128;
+constexpr uint32_t kSlab = 16384;     // 128 rows x 128 bytes
+constexpr int kThreads = 448;
+constexpr float kMaxSpan = 120.f;     // decay of a tile up to which its mask is one factor per column
+
+// A run of work of one CTA: n units from u0 on, of each the tiles [k0, k1) (k1 < 0:
+// all). from_cut: the state entering comes from the CTA before; to_cut: the state
+// left goes to the CTA behind (else to the unit's end state).
+struct Stage {
+    int u0, n, k0, k1;
+    int from_cut, to_cut;
+};
+
+// The part of a unit ahead of the cut behind a CTA: there is none (the cut falls
+// between units), it begins with the unit, it goes on from the cut before.
+enum { kLinkNone = -1, kLinkFirst = 0, kLinkNext = 1 };
+
+enum { kOrderHandoff = 0, kOrderNatural = 1, kOrderWhole = 2, kOrderState = 3 };
+
+struct TcParams {
+    const __nv_bfloat16 *dt;
+    long long dt_sb, dt_st;
+    const float *A, *D;
+    StepSize step;
+    const int *lens, *rows;          // (batch) lengths (-1: skipped row) and pages, or nullptr
+    const float *init;
+    float *state_out;
+    __nv_bfloat16 *out;
+    float *cut;                      // (CTAs, 64, N): the state at the cut behind CTA c
+    float *start;                    // (CTAs, 64, N): start state of the unit that the cut falls into, where its
+                                     // end state may be written before the CTA reads it
+    float *cut_decay;                // (CTAs) with kOrderState: decay of the part ahead of the cut
+    int2 *link;                      // (CTAs) with kOrderState: (kLink*, unit) of the part ahead of the cut
+    unsigned int *flags;             // (CTAs) with kOrderHandoff: cut[c] is there
+    DeviceStatus *status;
+    int batch, L, H, HU, heads_per_group, halves;   // HU = H P / 64 units a row, halves = P / 64
+    int order;
+};
+
+__device__ __forceinline__ int tiles_of(const TcParams &p, int b) {
+    const int len = p.lens ? p.lens[b] : p.L;
+    return len < 0 ? 0 : len == 0 ? 1 : (len + kTile - 1) / kTile;   // an empty sequence still passes its state on
+}
+
+// Where global tile g lies: unit u and tile k of it.
+struct Place {
+    int u, k;
+};
+
+// The stages of CTA c of nc and the number of its tiles; every thread of the block
+// calls it (`scratch`: blockDim.x + 8 entries of shared memory). With fewer tiles
+// than CTAs the last CTAs have none, so no share between two cuts is empty.
+__device__ void make_stages(const TcParams &p, int c, int nc, Stage *stages, int *nsteps, long long *scratch) {
+    const int tid = threadIdx.x, nth = blockDim.x;
+    long long *part = scratch;            // nth entries
+    Place *at = reinterpret_cast<Place *>(scratch + nth);      // 2
+    long long *total = scratch + nth + 2;
+    long long T;
+    if (p.order == kOrderWhole) {
+        if (tid == 0) {
+            const int nt = tiles_of(p, c / p.HU);
+            stages[0] = Stage{c, nt > 0 ? 1 : 0, 0, -1, 0, 0};
+            stages[1].n = stages[2].n = 0;
+            *nsteps = nt;
+        }
+        __syncthreads();
+        return;
+    }
+    long long lo, hi;
+    if (!p.lens) {
+        const int nt = tiles_of(p, 0);
+        T = (long long)p.batch * p.HU * nt;
+        if (nc > T) nc = (int)T;
+        lo = c < nc ? T * c / nc : T;
+        hi = c < nc ? T * (c + 1) / nc : T;
+        if (tid == 0) {
+            at[0] = Place{(int)(lo / nt), (int)(lo % nt)};
+            at[1] = Place{(int)(hi / nt), (int)(hi % nt)};
+        }
+    } else {
+        // sums of the rows' tiles: a run of rows per thread, then the runs
+        const int run = (p.batch + nth - 1) / nth, b0 = min(p.batch, tid * run), b1 = min(p.batch, b0 + run);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += tiles_of(p, b);
+        part[tid] = mine;
+        __syncthreads();
+        if (tid == 0) {
+            long long acc = 0;
+            for (int i = 0; i < nth; ++i) {
+                const long long v = part[i];
+                part[i] = acc;
+                acc += v;
+            }
+            *total = acc * p.HU;
+            at[0] = at[1] = Place{p.batch * p.HU, 0};
+        }
+        __syncthreads();
+        T = *total;
+        if (nc > T) nc = (int)T;
+        lo = c < nc ? T * c / nc : T;
+        hi = c < nc ? T * (c + 1) / nc : T;
+        long long acc = part[tid] * p.HU;
+        for (int b = b0; b < b1; ++b) {
+            const int nt = tiles_of(p, b);
+            const long long next = acc + (long long)nt * p.HU;
+            for (int q = 0; q < 2; ++q) {
+                const long long g = q ? hi : lo;
+                if (g >= acc && g < next) at[q] = Place{b * p.HU + (int)((g - acc) / nt), (int)((g - acc) % nt)};
+            }
+            acc = next;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const Place s = at[0], e = at[1];
+        Stage left{}, whole{}, right{};
+        if (lo < hi) {
+            if (s.u == e.u) {
+                right = Stage{s.u, 1, s.k, e.k, s.k > 0, 1};       // inside one unit, which goes on behind
+            } else {
+                if (s.k > 0) left = Stage{s.u, 1, s.k, -1, 1, 0};
+                const int first = s.u + (s.k > 0);
+                if (e.u > first) whole = Stage{first, e.u - first, 0, -1, 0, 0};
+                if (e.k > 0) right = Stage{e.u, 1, 0, e.k, 0, 1};
+            }
+        }
+        int n = (int)(hi - lo);
+        if (p.order == kOrderState) {
+            left.n = whole.n = 0;
+            right.from_cut = 0;
+            n = right.n ? right.k1 - right.k0 : 0;
+        }
+        const bool hand = p.order == kOrderHandoff;
+        stages[0] = hand ? right : left;
+        stages[1] = whole;
+        stages[2] = hand ? left : right;
+        *nsteps = n;
+    }
+    __syncthreads();
+}
+
+// A thread's walk over the tiles of its CTA.
+struct Walk {
+    const TcParams &p;
+    const Stage *st;
+    int s = 0, j = -1;
+    int u = 0, b = 0, len = 0, k = 0, k1 = 0;
+    bool first = false;            // the tile is its stage's unit's first
+    __device__ __forceinline__ Walk(const TcParams &p_, const Stage *st_) : p(p_), st(st_) {}
+    // the next unit with tiles; false behind the last
+    __device__ __forceinline__ bool unit() {
+        while (true) {
+            ++j;
+            while (s < 3 && j >= st[s].n) {
+                ++s;
+                j = 0;
+            }
+            if (s == 3) return false;
+            u = st[s].u0 + j;
+            b = u / p.HU;
+            len = p.lens ? p.lens[b] : p.L;
+            const int nt = len < 0 ? 0 : len == 0 ? 1 : (len + kTile - 1) / kTile;
+            if (nt == 0) continue;
+            k = st[s].k0;
+            k1 = st[s].k1 < 0 ? nt : st[s].k1;
+            first = true;
+            return true;
+        }
+    }
+    // the next tile
+    __device__ __forceinline__ bool tile() {
+        first = false;
+        return ++k < k1 ? true : unit();
+    }
+    __device__ __forceinline__ bool last() const { return k + 1 == k1; }
+    __device__ __forceinline__ int hu() const { return u % p.HU; }
+    // the state entering the tile is zero (no C H)
+    __device__ __forceinline__ bool zero_start() const { return first && !st[s].from_cut && (p.init == nullptr || p.order == kOrderState); }
+};
+
+template <int N, bool STATE>
+struct Layout {
+    static constexpr int kX = STATE ? 3 : 2;               // x slots
+    static constexpr uint32_t kBC = N * 256;               // bytes of a B or C tile
+    static constexpr uint32_t ring = 0;                    // 4 slots of 32 KB
+    static constexpr uint32_t x0 = 4 * 2 * kSlab;
+    static constexpr uint32_t h = x0 + kX * kSlab;         // bf16 (N, 64) state
+    static constexpr uint32_t xw = h + (STATE ? 0 : kSlab);   // the two terms of diag(w) X
+    static constexpr uint32_t small = xw + 2 * kSlab;
+};
+
+enum {
+    B_RING_FULL = 0, B_RING_EMPTY = 4, B_X_FULL = 8, B_X_EMPTY = 12,
+    B_G_READY = 16,      // 2: MMA -> group: G of the tile
+    B_M_READY = 18,      // 2: group -> MMA: M of the tile
+    B_Y_READY = 20,      // 2: MMA -> group (and C): Y and Yo of the tile
+    B_G_FREE = 22,       // 2: group -> MMA: the tile's TMEM buffers are read
+    B_VEC_READY = 24,    // 2: C -> group
+    B_VEC_FREE = 26,     // 2: group -> C
+    B_XW_READY = 28,     // C -> MMA
+    B_S_READY,           // MMA -> C
+    B_H_READY,           // C -> MMA
+    B_DONE,
+    B_COUNT
+};
+
+// Per-tile vectors from group C to groups A and B.
+struct TileVec {
+    float a[kTile], col[kTile], dt[kTile];
+};
+
+struct Small {
+    uint64_t bars[B_COUNT];
+    uint32_t tmem;
+    int abort_flag;
+    int nsteps;
+    int pad;
+    float red[2][8];
+    Stage stages[3];
+    alignas(16) TileVec vec[2];
+    long long scratch[kThreads + 8];
+};
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+typedef unsigned long long pair_t;
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t g0, uint32_t g1, float c0, float c1) {
+    pair_t g, c, m;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(g) : "r"(g0), "r"(g1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(m) : "l"(g), "l"(c));
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(m));
+    return pack_bf16x2(lo, hi);
+}
+
+// 32 bytes of one row of the output, in one store where the output is aligned to them.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool whole) {
+    if (!whole) {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Row `row` of diag(w) X as two bf16 terms; the x tile stays.
+__device__ __forceinline__ void split_row(const uint8_t *x, uint8_t *hi_tile, uint8_t *lo_tile, int row, float w) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(x + row * 128);
+    uint4 *hi = reinterpret_cast<uint4 *>(hi_tile + row * 128), *lo = reinterpret_cast<uint4 *>(lo_tile + row * 128);
+#pragma unroll 2
+    for (int k = 0; k < 8; ++k) {
+        const int c = (k + row) & 7;
+        uint4 v = src[c], l;
+        uint32_t *q = reinterpret_cast<uint32_t *>(&v), *ql = reinterpret_cast<uint32_t *>(&l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a0 = __uint_as_float(q[j] << 16) * w, a1 = __uint_as_float(q[j] & 0xffff0000u) * w;
+            const uint32_t t = pack_bf16x2(a0, a1);
+            ql[j] = pack_bf16x2(a0 - __uint_as_float(t << 16), a1 - __uint_as_float(t & 0xffff0000u));
+            q[j] = t;
+        }
+        hi[c] = v;
+        lo[c] = l;
+    }
+}
+__device__ __forceinline__ void zero_row(uint8_t *tile, int row) {
+    uint4 *d = reinterpret_cast<uint4 *>(tile + row * 128);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) d[(k + row) & 7] = make_uint4(0, 0, 0, 0);
+}
+
+template <int N, bool STATE>
+__global__ void __launch_bounds__(kThreads, 1)
+causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+                 const __grid_constant__ CUtensorMap tm_c, const TcParams p) {
+    using S = Layout<N, STATE>;
+    constexpr int NSLAB = N / 64;
+    constexpr int kX = S::kX;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *g = smem_raw + (base - smem_u32(smem_raw));
+    Small &sm = *reinterpret_cast<Small *>(g + S::small);
+    volatile int *abort_flag = &sm.abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
+
+    if (tid == 0) {
+        sm.abort_flag = 0;
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem), 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    make_stages(p, blockIdx.x, gridDim.x, sm.stages, &sm.nsteps, sm.scratch);
+    if (STATE && tid == 0) {
+        const Stage r = sm.stages[2];
+        p.link[blockIdx.x] = r.n ? make_int2(r.k0 ? kLinkNext : kLinkFirst, r.u0) : make_int2(kLinkNone, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t nsteps = (uint32_t)sm.nsteps;
+    auto tG = [&](uint32_t n) { return tmem + 128 * (n & 1); };          // G, then M in [0, 64) and Yo in [64, 128)
+    auto tY = [&](uint32_t n) { return tmem + 256 + 64 * (n & 1); };
+    auto tS = [&](uint32_t n) { return tmem + 384 + 64 * (n & 1); };
+    // ring slots and their use counts
+    auto slot_c = [](uint32_t n) { return (2 * n) & 3; };
+    auto slot_b = [](uint32_t n) { return STATE ? n & 3 : (2 * n + 1) & 3; };
+    auto use_bc = [](uint32_t n) { return STATE ? n >> 2 : n >> 1; };
+    auto slot_x = [](uint32_t n) { return n % kX; };
+    auto use_x = [](uint32_t n) { return n / kX; };
+    auto ring = [&](uint32_t s) { return base + S::ring + s * 2 * kSlab; };
+    auto xslot = [&](uint32_t n) { return S::x0 + slot_x(n) * kSlab; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&tm_x);
+            prefetch_tmap(&tm_b);
+            if (!STATE) prefetch_tmap(&tm_c);
+            Walk w(p, sm.stages);
+            uint32_t n = 0;
+            for (bool go = w.unit(); go && !*abort_flag; go = w.tile(), ++n) {
+                const int hu = w.hu(), grp = (hu / p.halves) / p.heads_per_group, t0 = w.k * kTile;
+                if (!STATE) {
+                    const uint32_t s = slot_c(n);
+                    if (n >= 2 && !mbar_wait_ool(bar(B_RING_EMPTY + s), (use_bc(n) - 1) & 1, abort_flag, p.status, 901)) break;
+                    mbar_arrive_expect_tx(bar(B_RING_FULL + s), S::kBC);
+                    for (int sl = 0; sl < NSLAB; ++sl)
+                        tma_load_4d(ring(s) + sl * kSlab, &tm_c, bar(B_RING_FULL + s), 64 * sl, grp, t0, w.b);
+                }
+                const uint32_t s = slot_b(n);
+                if (use_bc(n) >= 1 && !mbar_wait_ool(bar(B_RING_EMPTY + s), (use_bc(n) - 1) & 1, abort_flag, p.status, 902)) break;
+                mbar_arrive_expect_tx(bar(B_RING_FULL + s), S::kBC);
+                for (int sl = 0; sl < NSLAB; ++sl)
+                    tma_load_4d(ring(s) + sl * kSlab, &tm_b, bar(B_RING_FULL + s), 64 * sl, grp, t0, w.b);
+                const uint32_t xs = slot_x(n);
+                if (use_x(n) >= 1 && !mbar_wait_ool(bar(B_X_EMPTY + xs), (use_x(n) - 1) & 1, abort_flag, p.status, 903)) break;
+                mbar_arrive_expect_tx(bar(B_X_FULL + xs), kSlab);
+                tma_load_4d(base + xslot(n), &tm_x, bar(B_X_FULL + xs), 0, hu, t0, w.b);
+            }
+            // every load issued has landed before the CTA may exit: the last use of each slot
+            constexpr uint32_t kDeep = STATE ? 4 : 2;
+            for (uint32_t q = n > kDeep ? n - kDeep : 0; q < n; ++q) {
+                if (!STATE) mbar_drain(bar(B_RING_FULL + slot_c(q)), use_bc(q) & 1);
+                mbar_drain(bar(B_RING_FULL + slot_b(q)), use_bc(q) & 1);
+            }
+            for (uint32_t q = n > kX ? n - kX : 0; q < n; ++q) mbar_drain(bar(B_X_FULL + slot_x(q)), use_x(q) & 1);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_state = idesc_bf16_f32(128, 64, true, true);   // B^T (MN) x diag(w) X (MN)
+            constexpr uint32_t id_g = idesc_bf16_f32(128, 128, false, false);    // C (K) x B (K)
+            constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);      // C (K) x H (MN); M (K) x X (MN)
+            uint32_t nG = 0, nS = 0, nY = 0;
+            Walk w(p, sm.stages);            // at tile nY
+            if (nsteps) w.unit();
+            WaitClock clock;
+            uint32_t idle = 0;
+            while ((STATE ? nS : nY) < nsteps) {
+                bool moved = false;
+                // S(n) = B^T (hi + lo): group C has both terms; B has landed
+                if (nS < nsteps && mbar_test(bar(B_XW_READY), nS & 1) &&
+                    mbar_test(bar(B_RING_FULL + slot_b(nS)), use_bc(nS) & 1)) {
+                    tc_fence_after();
+                    const uint32_t sB = ring(slot_b(nS));
+#pragma unroll 1
+                    for (int q = 0; q < 2 * kTile / 16; ++q)
+                        mma_bf16_ss(tS(nS), sdesc_sw128(sB + (q & 7) * 2048, kSlab, 1024),
+                                    sdesc_sw128(base + S::xw + q * 2048, kSlab, 1024), id_state, q > 0);
+                    mma_commit(bar(B_S_READY));
+                    // B goes free with the second of its two readers, S and G
+                    if (STATE || nG > nS) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
+                    ++nS;
+                    moved = true;
+                }
+                if (!STATE) {
+                    // Y(n) = M X and Yo(n) = C H
+                    if (nY < nS && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1)) {
+                        tc_fence_after();
+                        const uint32_t sX = base + xslot(nY), sC = ring(slot_c(nY));
+#pragma unroll 1
+                        for (int q = 0; q < kTile / 16; ++q)
+                            mma_bf16_ts(tY(nY), tG(nY) + 8 * q, sdesc_sw128(sX + q * 2048, kSlab, 1024), id_o, q > 0);
+                        if (!w.zero_start()) {
+#pragma unroll 1
+                            for (int q = 0; q < N / 16; ++q)
+                                mma_bf16_ss(tG(nY) + 64, sdesc_sw128(sC + (q >> 2) * kSlab + (q & 3) * 32, 0, 1024),
+                                            sdesc_sw128(base + S::h + q * 2048, kSlab, 1024), id_o, q > 0);
+                        }
+                        mma_commit(bar(B_Y_READY + (nY & 1)));
+                        mma_commit(bar(B_RING_EMPTY + slot_c(nY)));
+                        ++nY;
+                        w.tile();
+                        moved = true;
+                    }
+                    // G(n) = C B^T: the operands have landed and tile n - 2's buffers are read
+                    if (nG < nsteps && mbar_test(bar(B_RING_FULL + slot_c(nG)), use_bc(nG) & 1) &&
+                        mbar_test(bar(B_RING_FULL + slot_b(nG)), use_bc(nG) & 1) &&
+                        (nG < 2 || mbar_test(bar(B_G_FREE + (nG & 1)), ((nG >> 1) - 1) & 1))) {
+                        tc_fence_after();
+                        const uint32_t sC = ring(slot_c(nG)), sB = ring(slot_b(nG));
+#pragma unroll 1
+                        for (int q = 0; q < N / 16; ++q) {
+                            const uint32_t ko = (q >> 2) * kSlab + (q & 3) * 32;
+                            mma_bf16_ss(tG(nG), sdesc_sw128(sC + ko, 0, 1024), sdesc_sw128(sB + ko, 0, 1024), id_g, q > 0);
+                        }
+                        mma_commit(bar(B_G_READY + (nG & 1)));
+                        if (nS > nG) mma_commit(bar(B_RING_EMPTY + slot_b(nG)));
+                        ++nG;
+                        moved = true;
+                    }
+                }
+                if (moved) {
+                    idle = 0;
+                    clock = WaitClock();
+                } else if ((++idle & 63u) == 0) {
+                    if (*abort_flag) break;
+                    if (clock.expired(1000000000ull)) {
+                        *abort_flag = 1;
+                        report_timeout(p.status, 910);
+                        break;
+                    }
+                }
+            }
+            // all MMAs complete before TMEM is released
+            mma_commit(bar(B_DONE));
+            mbar_drain(bar(B_DONE), 0);
+        }
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ group C
+        const int row = ((warp & 3) << 5) | lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) << 5) << 16;
+        float H[64];
+        uint32_t raw = 0;
+        auto load_dt = [&](const Walk &w, bool there) {
+            raw = 0;
+            const int t = w.k * kTile + row;
+            if (there && t < w.len) {
+                const __nv_bfloat16 *q = p.dt + (long long)w.b * p.dt_sb + (long long)t * p.dt_st + w.hu() / p.halves;
+                asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(raw) : "l"(q));
+            }
+        };
+        // the state behind a stage's unit, to the unit's end state or to the cut
+        auto sink = [&](int u, int b, bool to_cut, float decay) {
+            if (to_cut && p.order == kOrderNatural) return;      // the chain has put it there
+            if (row < N && !*abort_flag) {
+                float *d = nullptr;
+                if (to_cut) d = p.cut + (size_t)blockIdx.x * 64 * N;
+                else if (p.state_out) d = p.state_out + ((size_t)(p.rows ? p.rows[b] : b) * p.HU + u % p.HU) * 64 * N;
+                if (d) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) d[(size_t)j * N + row] = H[j];
+                }
+            }
+            if (to_cut) {
+                sync_c();
+                if (row == 0) {
+                    if (STATE) p.cut_decay[blockIdx.x] = decay;
+                    else if (p.order == kOrderHandoff && !*abort_flag) flag_release(p.flags + blockIdx.x, 1u);
+                }
+            }
+        };
+        Walk w(p, sm.stages), ahead(p, sm.stages);
+        bool go = w.unit();
+        bool more = ahead.unit();
+        load_dt(ahead, more);
+        uint32_t n = 0;
+        float gprev = 0.f, gall = 1.f;       // exp(A * sum of dt) of the previous tile, of the stage so far
+        int pu = 0, pb = 0;
+        bool pend = false, pcut = false;     // the previous tile ended its unit or stage
+        // H <- exp(A sum dt) H + S of tile m
+        auto advance = [&](uint32_t m) {
+            tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t sv[32];
+                tmem_ld32(tS(m) + lane_off + half * 32, sv);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) H[half * 32 + j] = fmaf(gprev, H[half * 32 + j], __uint_as_float(sv[j]));
+            }
+            tc_fence_before();
+        };
+        // an aborted CTA walks on to its end (its waits return at once): a group's
+        // threads never part ways ahead of their barriers
+#pragma unroll 1
+        for (; go; go = w.tile(), ++n) {
+            const int valid = w.len - w.k * kTile;       // rows of the tile that hold tokens
+            const int h = w.hu() / p.halves;
+            const float A = p.A[h];
+            const float v = row < valid ? p.step(bf2f(raw), h) : 0.f;
+            if (more) more = ahead.tile();
+            load_dt(ahead, more);
+            // sums of dt up to and with the row, and behind it
+            float pf = v, sf = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, pf, o), dn = __shfl_down_sync(0xffffffffu, sf, o);
+                if (lane >= o) pf += up;
+                if (lane + o < 32) sf += dn;
+            }
+            float *red = sm.red[n & 1];
+            if (lane == 31) red[row >> 5] = pf;
+            sync_c();
+            float ahead_sum = 0.f, behind = 0.f, tot = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q < (row >> 5)) ahead_sum += red[q];
+                if (q > (row >> 5)) behind += red[q];
+            }
+            tot = (red[0] + red[1]) + (red[2] + red[3]);
+            // a row's weight in the state: the sum behind it, added up from the end
+            const float weight = expf(A * ((sf - v) + behind)) * v;
+            if (!STATE) {
+                const float my_a = A * (ahead_sum + pf);
+                const uint32_t vb = n & 1;
+                if (n >= 2) mbar_wait_ool(bar(B_VEC_FREE + vb), ((n >> 1) - 1) & 1, abort_flag, p.status, 920);
+                TileVec &V = sm.vec[vb];
+                V.a[row] = my_a;
+                V.dt[row] = v;
+                V.col[row] = __expf(0.5f * A * tot - my_a) * v;
+                sync_c();
+                if (row == 0) mbar_arrive(bar(B_VEC_READY + vb));
+            }
+            // diag(w) X in two terms, once S of the tile before has read its buffers
+            mbar_wait_ool(bar(B_X_FULL + slot_x(n)), use_x(n) & 1, abort_flag, p.status, 921);
+            if (n >= 1) mbar_wait_ool(bar(B_S_READY), (n - 1) & 1, abort_flag, p.status, 922);
+            uint8_t *xt = g + xslot(n);
+            if (row < valid) {
+                split_row(xt, g + S::xw, g + S::xw + kSlab, row, weight);
+            } else {
+                // what lies behind the sequence may be anything: zero it wherever a product
+                // sums over it (x, diag(w) X, B)
+                zero_row(g + S::xw, row);
+                zero_row(g + S::xw + kSlab, row);
+                zero_row(xt, row);
+                mbar_wait_ool(bar(B_RING_FULL + slot_b(n)), use_bc(n) & 1, abort_flag, p.status, 923);
+                for (int sl = 0; sl < NSLAB; ++sl) zero_row(g + S::ring + slot_b(n) * 2 * kSlab + sl * kSlab, row);
+            }
+            fence_proxy_async_smem();
+            sync_c();
+            if (row == 0) {
+                mbar_arrive(bar(B_XW_READY));
+                if (STATE) mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
+            }
+            // the state entering the tile
+            if (n >= 1) advance(n - 1);
+            if (pend) sink(pu, pb, pcut, gall);
+            if (w.first) {
+                gall = 1.f;
+                const float *from = nullptr;
+                if (!STATE) {
+                    if (w.st[w.s].from_cut) {
+                        from = p.cut + (size_t)(blockIdx.x - 1) * 64 * N;
+                        if (p.order == kOrderHandoff) {
+                            if (row == 0) flag_wait(p.flags + blockIdx.x - 1, 1u, abort_flag, p.status, 924);
+                            sync_c();
+                        }
+                    } else if (p.init && p.order == kOrderNatural && w.st[w.s].to_cut) {
+                        from = p.start + (size_t)blockIdx.x * 64 * N;
+                    } else if (p.init) {
+                        from = p.init + ((size_t)(p.rows ? p.rows[w.b] : w.b) * p.HU + w.hu()) * 64 * N;
+                    }
+                }
+                if (from && row < N) {
+                    // another CTA of this launch may have written it: past L1
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) H[j] = __ldcg(from + (size_t)j * N + row);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) H[j] = 0.f;
+                }
+            }
+            if (!STATE) {
+                // C H of the tile before has read the buffer
+                if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 925);
+                if (row < N && !w.zero_start()) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, c)) =
+                            make_uint4(pack_bf16x2(H[8 * c], H[8 * c + 1]), pack_bf16x2(H[8 * c + 2], H[8 * c + 3]),
+                                       pack_bf16x2(H[8 * c + 4], H[8 * c + 5]), pack_bf16x2(H[8 * c + 6], H[8 * c + 7]));
+                }
+                fence_proxy_async_smem();
+                sync_c();
+                if (row == 0) mbar_arrive(bar(B_H_READY));
+            }
+            gprev = expf(A * tot);
+            gall *= gprev;
+            pend = w.last();
+            pu = w.u;
+            pb = w.b;
+            pcut = w.st[w.s].to_cut;
+        }
+        if (n >= 1) {
+            mbar_wait_ool(bar(B_S_READY), (n - 1) & 1, abort_flag, p.status, 926);
+            advance(n - 1);
+            if (pend) sink(pu, pb, pcut, gall);
+        }
+    } else if (!STATE) {
+        // ------------------------------------------------------------ groups A and B
+        const bool is_b = warp >= 10;
+        const int row = ((warp & 3) << 5) | lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) << 5) << 16;
+        const int wq = warp & 3;
+        auto sync_g = [&]() { if (is_b) sync_b(); else sync_a(); };
+        Walk w(p, sm.stages);
+        bool go = w.unit();
+        if (is_b && go) go = w.tile();
+        uint32_t n = is_b ? 1 : 0;
+#pragma unroll 1
+        for (; go; n += 2) {
+            const uint32_t par = (n >> 1) & 1, vb = n & 1;
+            // ---------------- the mask
+            mbar_wait_ool(bar(B_VEC_READY + vb), par, abort_flag, p.status, 930);
+            const TileVec &V = sm.vec[vb];
+            const float my_a = V.a[row], all = V.a[kTile - 1];
+            const bool one_factor = all > -kMaxSpan;
+            mbar_wait_ool(bar(B_G_READY + vb), par, abort_flag, p.status, 931);
+            tc_fence_after();
+            const uint32_t tg = tG(n) + lane_off;
+#pragma unroll 1
+            for (int J = 0; J < 4; ++J) {
+                uint32_t m[16];
+                if (J > wq) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) m[q] = 0u;
+                } else {
+                    uint32_t gv[32];
+                    tmem_ld32(tg + J * 32, gv);
+                    tmem_wait_ld();
+                    const int s0 = J * 32;
+                    if (one_factor) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 4) {
+                            const float4 c = *reinterpret_cast<const float4 *>(&V.col[s0 + q]);
+                            m[q / 2] = scaled_pair(gv[q], gv[q + 1], c.x, c.y);
+                            m[q / 2 + 1] = scaled_pair(gv[q + 2], gv[q + 3], c.z, c.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 2) {
+                            const float e0 = __expf(fminf(my_a - V.a[s0 + q], 0.f)) * V.dt[s0 + q];
+                            const float e1 = __expf(fminf(my_a - V.a[s0 + q + 1], 0.f)) * V.dt[s0 + q + 1];
+                            m[q / 2] = scaled_pair(gv[q], gv[q + 1], e0, e1);
+                        }
+                    }
+                    if (J == wq) {
+                        // entries behind the row's own token are dropped, never multiplied
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            m[q] = 2 * q + 1 <= lane ? m[q] : 2 * q <= lane ? (m[q] & 0xffffu) : 0u;
+                    }
+                }
+                // columns [32 J, 32 J + 32) of M as 16 words over G columns already read
+                tmem_st16(tg + J * 16, m);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            sync_g();
+            if (row == 0) {
+                mbar_arrive(bar(B_M_READY + vb));
+                mbar_arrive(bar(B_VEC_FREE + vb));
+            }
+            // ---------------- the output
+            const int t = w.k * kTile + row;
+            const bool zs = w.zero_start();
+            const float rf = one_factor ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a);
+            const int hu = w.hu();
+            const float D = p.D ? p.D[hu / p.halves] : 0.f;
+            __nv_bfloat16 *dst = p.out + (((size_t)w.b * p.L + t) * p.HU + hu) * 64;
+            const uint8_t *xt = g + xslot(n);
+            mbar_wait_ool(bar(B_Y_READY + vb), par, abort_flag, p.status, 932);
+            tc_fence_after();
+            const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+            const bool store = t < p.L && !*abort_flag, keep = t < w.len;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t yv[16], ov[16], o8[8];
+                tmem_ld16(tY(n) + lane_off + q * 16, yv);
+                if (zs) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) ov[c] = 0u;
+                } else {
+                    tmem_ld16(tG(n) + 64 + lane_off + q * 16, ov);
+                }
+                uint4 xv[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) xv[c] = *reinterpret_cast<const uint4 *>(xt + sw128_offset(row, q * 2 + c));
+                const uint32_t *xu = reinterpret_cast<const uint32_t *>(xv);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float x0 = __uint_as_float(xu[c] << 16), x1 = __uint_as_float(xu[c] & 0xffff0000u);
+                    const float y0 = fmaf(rf, __uint_as_float(yv[2 * c]), fmaf(e, __uint_as_float(ov[2 * c]), D * x0));
+                    const float y1 = fmaf(rf, __uint_as_float(yv[2 * c + 1]), fmaf(e, __uint_as_float(ov[2 * c + 1]), D * x1));
+                    o8[c] = keep ? pack_bf16x2(y0, y1) : 0u;
+                }
+                if (store) store32(dst + q * 16, o8, whole);
+            }
+            tc_fence_before();
+            sync_g();
+            if (row == 0) {
+                mbar_arrive(bar(B_G_FREE + vb));
+                mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
+            }
+            go = w.tile();
+            if (go) go = w.tile();
+        }
+    }
+
+    // ------------------------------------------------------------ teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// The chain of states across the cuts: cut[c] holds the own end state (from zero)
+// of the part ahead of the cut behind CTA c, cut_decay[c] its decay; they become
+// the states at the cuts, in place. A block takes 256 x 4 elements of the chain
+// that begins with CTA c.
+template <int N>
+__global__ void __launch_bounds__(256) causal_chain_kernel(const TcParams p, int nc) {
+    constexpr int kParts = 64 * N / 1024;
+    constexpr size_t kState = 64 * N / 4;
+    const int c0 = blockIdx.x / kParts, e = (blockIdx.x % kParts) * 256 + threadIdx.x;
+    const int2 first = p.link[c0];
+    if (first.x != kLinkFirst) return;
+    const int u = first.y, b = u / p.HU;
+    // the CTAs that go on from here
+    int end = c0 + 1;
+    for (bool more = true; more;) {
+        const int c = end + (threadIdx.x & 31);
+        const unsigned go = __ballot_sync(0xffffffffu, c < nc && p.link[c < nc ? c : 0].x == kLinkNext);
+        const int run = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+        end += run;
+        more = run == 32;
+    }
+    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.init) h = reinterpret_cast<const float4 *>(p.init + ((size_t)(p.rows ? p.rows[b] : b) * p.HU + u % p.HU) * 64 * N)[e];
+    // the unit's last part may end, in place, before its first part begins
+    if (p.init) reinterpret_cast<float4 *>(p.start)[c0 * kState + e] = h;
+    float4 *cut = reinterpret_cast<float4 *>(p.cut) + e;
+    constexpr int kAhead = 8;              // loads in flight
+    for (int c = c0; c < end; c += kAhead) {
+        float4 own[kAhead];
+        float d[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (c + q < end) {
+                own[q] = cut[(size_t)(c + q) * kState];
+                d[q] = p.cut_decay[c + q];
+            }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (c + q < end) {
+                h = make_float4(fmaf(d[q], h.x, own[q].x), fmaf(d[q], h.y, own[q].y), fmaf(d[q], h.z, own[q].z),
+                                fmaf(d[q], h.w, own[q].w));
+                cut[(size_t)(c + q) * kState] = h;
+            }
+    }
+}
+
+// Rows of a ragged or paged batch: resolved pages, effective lengths (-1: skipped)
+// and the zeros of the output rows that no tile covers. Block (b, part).
+__global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, int *rows, int *lens) {
+    const int b = blockIdx.x;
+    int row = b;
+    bool bad = false;
+    if (a.slots) {
+        row = a.slots[b];
+        bad = row < -1 || row >= a.nslots;
+        bool again = false;
+        if (row >= 0)
+            for (int i = threadIdx.x; i < b; i += 128) again |= a.slots[i] == row;
+        bad |= (bool)__syncthreads_or(again);
+        if (bad) row = -1;
+    }
+    const int len = row < 0 ? -1 : a.len(b);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        rows[b] = row;
+        lens[b] = len;
+        if (bad) atomicOr(&a.status->flags, kFlagIndex);
+    }
+    const int covered = len < 0 ? 0 : len == 0 ? kTile : (len + kTile - 1) / kTile * kTile;
+    if (covered >= a.L) return;
+    const size_t row16 = (size_t)a.H * a.P / 8;       // 16-byte pieces of a token
+    uint4 *out = static_cast<uint4 *>(a.out) + ((size_t)b * a.L + covered) * row16;
+    const size_t n = (size_t)(a.L - covered) * row16;
+    for (size_t i = (size_t)blockIdx.y * 128 + threadIdx.x; i < n; i += (size_t)gridDim.y * 128) out[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Scratch of the path behind the status header.
+struct TcScratch {
+    size_t rows, lens, flags, link, decay, cut, start, total;
+};
+TcScratch tc_scratch(int batch, int sms, int N) {
+    TcScratch s{};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    s.rows = take(sizeof(int) * (size_t)batch);
+    s.lens = take(sizeof(int) * (size_t)batch);
+    s.flags = take(sizeof(int) * (size_t)sms);
+    s.link = take(sizeof(int2) * (size_t)sms);
+    s.decay = take(sizeof(float) * (size_t)sms);
+    s.cut = take(sizeof(float) * (size_t)sms * 64 * N);
+    s.start = take(sizeof(float) * (size_t)sms * 64 * N);
+    s.total = o;
+    return s;
+}
+
+bool map_rows(CUtensorMap *m, const void *base, int inner, int count, int L, int batch, long long token, long long row) {
+    uint64_t dims[4] = {(uint64_t)inner, (uint64_t)count, (uint64_t)L, (uint64_t)batch};
+    uint64_t str[3] = {(uint64_t)inner * 2, (uint64_t)token * 2, (uint64_t)row * 2};
+    uint32_t box[4] = {64, 1, kTile, 1};
+    return tmap::make_map(m, base, 4, dims, str, box);
+}
+
+template <int N, bool STATE>
+cudaError_t launch_tc(const CUtensorMap &x, const CUtensorMap &b, const CUtensorMap &c, const TcParams &p, int ctas,
+                      cudaStream_t stream) {
+    auto k = causal_tc_kernel<N, STATE>;
+    const size_t smem = Layout<N, STATE>::small + sizeof(Small) + 1024;
+    static_assert(Layout<N, STATE>::small + sizeof(Small) + 1024 <= 232448, "shared memory of a CTA");
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k<<<ctas, kThreads, smem, stream>>>(x, b, c, p);
+    return cudaGetLastError();
+}
+
+template <int N>
+cudaError_t run_tc(const CausalArgs &a, void *scratch, cudaStream_t stream) {
+    const int sms = device_sms();
+    if (sms < 1 || !tmap::encode_fn()) return cudaErrorNotSupported;
+    const TcScratch t = tc_scratch(a.batch, sms, N);
+    char *ws = static_cast<char *>(scratch);
+    cudaError_t e;
+    TcParams p{};
+    p.dt = static_cast<const __nv_bfloat16 *>(a.dt);
+    p.dt_sb = a.dt_sb; p.dt_st = a.dt_st;
+    p.A = a.A; p.D = a.D; p.step = a.step;
+    p.init = a.init; p.state_out = a.state_out; p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.cut = reinterpret_cast<float *>(ws + t.cut);
+    p.start = reinterpret_cast<float *>(ws + t.start);
+    p.cut_decay = reinterpret_cast<float *>(ws + t.decay);
+    p.link = reinterpret_cast<int2 *>(ws + t.link);
+    p.flags = reinterpret_cast<unsigned int *>(ws + t.flags);
+    p.status = a.status;
+    p.batch = a.batch; p.L = a.L; p.H = a.H;
+    p.halves = a.P / 64; p.HU = a.H * p.halves; p.heads_per_group = a.H / a.G;
+    if (a.seqlens || a.slots) {
+        int *rows = reinterpret_cast<int *>(ws + t.rows), *lens = reinterpret_cast<int *>(ws + t.lens);
+        // enough blocks a row to zero a long tail, few where the rows are many
+        const int parts = 8 * sms / a.batch;
+        causal_rows_kernel<<<dim3(a.batch, parts < 1 ? 1 : parts > 64 ? 64 : parts), 128, 0, stream>>>(a, rows, lens);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        p.rows = rows;
+        p.lens = lens;
+    }
+    CUtensorMap tx, tb, tc;
+    if (!map_rows(&tx, a.x, 64, p.HU, a.L, a.batch, a.x_st, a.x_sb) ||
+        !map_rows(&tb, a.B, N, a.G, a.L, a.batch, a.b_st, a.b_sb) || !map_rows(&tc, a.C, N, a.G, a.L, a.batch, a.c_st, a.c_sb))
+        return cudaErrorInvalidValue;
+    const long long units = (long long)a.batch * p.HU, nt = (a.L + kTile - 1) / kTile;
+    if (units >= sms) {
+        p.order = kOrderHandoff;
+        if ((e = cudaMemsetAsync(p.flags, 0, sizeof(int) * (size_t)sms, stream)) != cudaSuccess) return e;
+        return launch_tc<N, false>(tx, tb, tc, p, sms, stream);
+    }
+    // fewer units than SMs: the cut work costs a second pass over x and B and two
+    // more launches, but spreads over every SM
+    const long long share = (units * nt + sms - 1) / sms;
+    if (10 * nt > 16 * share + 60) {
+        p.order = kOrderState;
+        if ((e = launch_tc<N, true>(tx, tb, tc, p, sms, stream)) != cudaSuccess) return e;
+        causal_chain_kernel<N><<<sms * (64 * N / 1024), 256, 0, stream>>>(p, sms);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        p.order = kOrderNatural;
+        return launch_tc<N, false>(tx, tb, tc, p, sms, stream);
+    }
+    p.order = kOrderWhole;
+    return launch_tc<N, false>(tx, tb, tc, p, (int)units, stream);
+}
+
+}  // namespace
+
+size_t causal_tc_scratch_bytes(int batch, int N) {
+    const int sms = device_sms();
+    return tc_scratch(batch, sms > 0 ? sms : 148, N).total;
+}
+
+cudaError_t launch_causal_tc(const CausalArgs &a, void *scratch, cudaStream_t stream) {
+    return a.N == 128 ? run_tc<128>(a, scratch, stream) : run_tc<64>(a, scratch, stream);
+}
+
+}  // namespace ssd

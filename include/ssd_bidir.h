@@ -430,7 +430,11 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
  *   state_out pool fp32, nullable (the end states are not wanted)
  * Within a sequence a non-finite input makes the outputs of its own tile of 128
  * tokens undefined, not only those behind it.
- * path: SSD_PATH_AUTO or SSD_PATH_SIMT (the CUDA-core scan). Workspace:
+ * path: SSD_PATH_AUTO, SSD_PATH_SIMT (the CUDA-core scan, either dtype) or
+ * SSD_PATH_FUSED (the tensor-core kernel, bf16; what AUTO takes for bf16). With
+ * bf16 the state is carried and returned in fp32 with fp32 accuracy on either
+ * path; on the tensor cores the masked C.B^T tile and the copy of the state
+ * that the outputs read are rounded to bf16. Workspace:
  * ssd_workspace_bytes with SSD_OP_CAUSAL_FWD (chunk is ignored). */
 int ssd_causal_fwd(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,
                    const float *dt_bias, float dt_min, float dt_max, const int *seqlens, const int *slots,

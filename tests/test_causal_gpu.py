@@ -95,7 +95,7 @@ SHAPES = [
 
 
 def paths_of(ssd, io):
-    return [ssd.SSD_PATH_AUTO]
+    return [ssd.SSD_PATH_AUTO] + ([ssd.SSD_PATH_SIMT] if io == "bf16" else [])
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_L%d_H%d_P%d_N%d_G%d_%s_%d%d%d%d" % s)
