@@ -17,8 +17,12 @@ struct StepSize {
     const float *bias;   // (H) or nullptr: the step size is used as given
     float lo, hi;
     __device__ __forceinline__ float operator()(float v, int h) const {
+        return with(v, bias ? bias[h] : 0.f);
+    }
+    // the same with the head's bias at hand
+    __device__ __forceinline__ float with(float v, float b) const {
         if (!bias) return v;
-        const float u = v + bias[h];
+        const float u = v + b;
         const float s = u > 20.f ? u : log1pf(expf(u));
         return fminf(fmaxf(s, lo), hi);
     }

@@ -18,8 +18,8 @@
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
 // products whose result is rounded to bf16 (relative 2^-9 a term, random). The
-// state is a result in fp32, so diag(w) X enters S as two bf16 terms, the rounded
-// product and its remainder (relative 2^-18 a term), and H stays in fp32 registers.
+// state is a result in fp32, so diag(w) X enters S as three bf16 terms (24 bits),
+// and H stays in fp32 registers.
 //
 // What bounds it: HBM (x, B, C and y once). Work is cut so that every CTA has
 // the same number of tiles: the tiles of all units in order, divided evenly. A
@@ -29,14 +29,16 @@
 // before it is wanted. With fewer units (long sequences) a pass over x and B gives
 // every part's own end state, a small kernel chains them, and the outputs follow.
 //
-// Roles (448 threads): warp 0 TMA producer; warp 1 MMA issuer, which polls what
-// is ready (S, then Y and Yo, then G) instead of waiting in a fixed order; warps
-// 2..5 group C: decays, diag(w) X, the state; warps 6..9 and 10..13 groups A and B:
+// Roles (640 threads): warp 0 TMA producer; warp 1 MMA issuer, which polls what
+// is ready (S, then Y and Yo, then G) instead of waiting in a fixed order; warp 2
+// the decays of the coming tiles (up to four ahead) and what else is to be known
+// of them; warps 4..11 group C: diag(w) X by halves of a tile, and the state,
+// rows n of it a thread, 32 columns each; warps 12..15 and 16..19 groups A and B:
 // mask and output of the even and the odd tiles, so that one tile's mask overlaps
-// the other's products and output. In a group, thread r owns tile row r.
+// the other's products and output; thread r owns tile row r.
 // TMEM (512 columns): two of {G 128: M packed over its first half once read, Yo over
-// its second}, two Y, two S. Shared memory: C and B two tiles deep, x two, H and
-// the two terms of diag(w) X once.
+// its second}, two Y, two S. Shared memory: C and B two tiles deep, x two, H once,
+// the three terms of half a tile of diag(w) X.
 // Every wait is bounded; one that expires sets the workspace's timeout flag and
 // the CTA runs to its end without storing.
 #include <cuda.h>
@@ -56,7 +58,10 @@ using namespace fused;
 
 constexpr int kTile = 128;
 constexpr uint32_t kSlab = 16384;     // 128 rows x 128 bytes
-constexpr int kThreads = 448;
+constexpr int kThreads = 640;
+constexpr int kStateThreads = 384;    // without groups A and B
+constexpr int kVec = 4;               // tiles whose decays are kept
+constexpr uint32_t kHalf = 8192;      // 64 rows x 128 bytes
 constexpr float kMaxSpan = 120.f;     // decay of a tile up to which its mask is one factor per column
 
 // A run of work of one CTA: n units from u0 on, of each the tiles [k0, k1) (k1 < 0:
@@ -200,8 +205,8 @@ struct Walk {
     const TcParams &p;
     const Stage *st;
     int s = 0, j = -1;
-    int u = 0, b = 0, len = 0, k = 0, k1 = 0;
-    bool first = false;            // the tile is its stage's unit's first
+    int b = 0, hu = 0, h = 0, len = 0, k = 0, k1 = 0;
+    bool first = false;            // the tile is the first of its unit's here
     __device__ __forceinline__ Walk(const TcParams &p_, const Stage *st_) : p(p_), st(st_) {}
     // the next unit with tiles; false behind the last
     __device__ __forceinline__ bool unit() {
@@ -212,8 +217,14 @@ struct Walk {
                 j = 0;
             }
             if (s == 3) return false;
-            u = st[s].u0 + j;
-            b = u / p.HU;
+            if (j == 0) {
+                b = st[s].u0 / p.HU;
+                hu = st[s].u0 % p.HU;
+            } else if (++hu == p.HU) {
+                hu = 0;
+                ++b;
+            }
+            h = hu / p.halves;
             len = p.lens ? p.lens[b] : p.L;
             const int nt = len < 0 ? 0 : len == 0 ? 1 : (len + kTile - 1) / kTile;
             if (nt == 0) continue;
@@ -228,10 +239,6 @@ struct Walk {
         first = false;
         return ++k < k1 ? true : unit();
     }
-    __device__ __forceinline__ bool last() const { return k + 1 == k1; }
-    __device__ __forceinline__ int hu() const { return u % p.HU; }
-    // the state entering the tile is zero (no C H)
-    __device__ __forceinline__ bool zero_start() const { return first && !st[s].from_cut && (p.init == nullptr || p.order == kOrderState); }
 };
 
 template <int N, bool STATE>
@@ -241,8 +248,8 @@ struct Layout {
     static constexpr uint32_t ring = 0;                    // 4 slots of 32 KB
     static constexpr uint32_t x0 = 4 * 2 * kSlab;
     static constexpr uint32_t h = x0 + kX * kSlab;         // bf16 (N, 64) state
-    static constexpr uint32_t xw = h + (STATE ? 0 : kSlab);   // the two terms of diag(w) X
-    static constexpr uint32_t small = xw + 2 * kSlab;
+    static constexpr uint32_t xw = h + (STATE ? 0 : kSlab);   // the three terms of half a tile of diag(w) X
+    static constexpr uint32_t small = xw + 3 * kHalf;
 };
 
 enum {
@@ -251,18 +258,23 @@ enum {
     B_M_READY = 18,      // 2: group -> MMA: M of the tile
     B_Y_READY = 20,      // 2: MMA -> group (and C): Y and Yo of the tile
     B_G_FREE = 22,       // 2: group -> MMA: the tile's TMEM buffers are read
-    B_VEC_READY = 24,    // 2: C -> group
-    B_VEC_FREE = 26,     // 2: group -> C
-    B_XW_READY = 28,     // C -> MMA
-    B_S_READY,           // MMA -> C
+    B_VEC_READY = 24,    // kVec: warp 2 -> groups
+    B_VEC_FREE = 28,     // kVec: C and the tile's group -> warp 2
+    B_XW_READY = 32,     // C -> MMA, twice a tile
+    B_S_READY,           // MMA -> C, twice a tile
     B_H_READY,           // C -> MMA
     B_DONE,
     B_COUNT
 };
 
-// Per-tile vectors from group C to groups A and B.
-struct TileVec {
-    float a[kTile], col[kTile], dt[kTile];
+// What is known of a tile, from warp 2 to the other warps: a_s, the column
+// factors of M (the step sizes where each entry takes its own exponential), the
+// weights in the state.
+enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32 };
+struct TileInfo {
+    float a[kTile], col[kTile], w[kTile];
+    int b, h, hu, t0, len, flags;
+    float decay, D;      // exp(a_T); the head's skip factor
 };
 
 struct Small {
@@ -271,9 +283,8 @@ struct Small {
     int abort_flag;
     int nsteps;
     int pad;
-    float red[2][8];
     Stage stages[3];
-    alignas(16) TileVec vec[2];
+    alignas(16) TileInfo info[kVec];
     long long scratch[kThreads + 8];
 };
 
@@ -312,34 +323,26 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool wh
                  : "memory");
 }
 
-// Row `row` of diag(w) X as two bf16 terms; the x tile stays.
-__device__ __forceinline__ void split_row(const uint8_t *x, uint8_t *hi_tile, uint8_t *lo_tile, int row, float w) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(x + row * 128);
-    uint4 *hi = reinterpret_cast<uint4 *>(hi_tile + row * 128), *lo = reinterpret_cast<uint4 *>(lo_tile + row * 128);
-#pragma unroll 2
-    for (int k = 0; k < 8; ++k) {
-        const int c = (k + row) & 7;
-        uint4 v = src[c], l;
-        uint32_t *q = reinterpret_cast<uint32_t *>(&v), *ql = reinterpret_cast<uint32_t *>(&l);
+// 16 bytes (8 values) of a row of diag(w) X as three bf16 terms, which carry 24
+// bits of each product.
+__device__ __forceinline__ void split3(uint4 x, float w, uint4 (&t)[3]) {
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(&x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a0 = __uint_as_float(q[j] << 16) * w, a1 = __uint_as_float(q[j] & 0xffff0000u) * w;
-            const uint32_t t = pack_bf16x2(a0, a1);
-            ql[j] = pack_bf16x2(a0 - __uint_as_float(t << 16), a1 - __uint_as_float(t & 0xffff0000u));
-            q[j] = t;
+    for (int j = 0; j < 4; ++j) {
+        float a0 = __uint_as_float(q[j] << 16) * w, a1 = __uint_as_float(q[j] & 0xffff0000u) * w;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t r = pack_bf16x2(a0, a1);
+            reinterpret_cast<uint32_t *>(&t[k])[j] = r;
+            a0 -= __uint_as_float(r << 16);
+            a1 -= __uint_as_float(r & 0xffff0000u);
         }
-        hi[c] = v;
-        lo[c] = l;
     }
 }
-__device__ __forceinline__ void zero_row(uint8_t *tile, int row) {
-    uint4 *d = reinterpret_cast<uint4 *>(tile + row * 128);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) d[(k + row) & 7] = make_uint4(0, 0, 0, 0);
-}
+__device__ __forceinline__ void sync_state() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int N, bool STATE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(STATE ? kStateThreads : kThreads, 1)
 causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                  const __grid_constant__ CUtensorMap tm_c, const TcParams p) {
     using S = Layout<N, STATE>;
@@ -355,7 +358,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 
     if (tid == 0) {
         sm.abort_flag = 0;
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < B_COUNT; ++i)
+            mbar_init(bar(i), !STATE && i >= B_VEC_FREE && i < B_VEC_FREE + kVec ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -394,7 +398,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             Walk w(p, sm.stages);
             uint32_t n = 0;
             for (bool go = w.unit(); go && !*abort_flag; go = w.tile(), ++n) {
-                const int hu = w.hu(), grp = (hu / p.halves) / p.heads_per_group, t0 = w.k * kTile;
+                const int grp = w.h / p.heads_per_group, t0 = w.k * kTile;
                 if (!STATE) {
                     const uint32_t s = slot_c(n);
                     if (n >= 2 && !mbar_wait_ool(bar(B_RING_EMPTY + s), (use_bc(n) - 1) & 1, abort_flag, p.status, 901)) break;
@@ -410,7 +414,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 const uint32_t xs = slot_x(n);
                 if (use_x(n) >= 1 && !mbar_wait_ool(bar(B_X_EMPTY + xs), (use_x(n) - 1) & 1, abort_flag, p.status, 903)) break;
                 mbar_arrive_expect_tx(bar(B_X_FULL + xs), kSlab);
-                tma_load_4d(base + xslot(n), &tm_x, bar(B_X_FULL + xs), 0, hu, t0, w.b);
+                tma_load_4d(base + xslot(n), &tm_x, bar(B_X_FULL + xs), 0, w.hu, t0, w.b);
             }
             // every load issued has landed before the CTA may exit: the last use of each slot
             constexpr uint32_t kDeep = STATE ? 4 : 2;
@@ -426,46 +430,53 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             constexpr uint32_t id_state = idesc_bf16_f32(128, 64, true, true);   // B^T (MN) x diag(w) X (MN)
             constexpr uint32_t id_g = idesc_bf16_f32(128, 128, false, false);    // C (K) x B (K)
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);      // C (K) x H (MN); M (K) x X (MN)
-            uint32_t nG = 0, nS = 0, nY = 0;
-            Walk w(p, sm.stages);            // at tile nY
-            if (nsteps) w.unit();
+            // descriptors of the fixed buffers and of ring and x slot 0: another slot,
+            // and a K step, only add to the start address (in 16-byte units)
+            const uint64_t mn = sdesc_sw128(base, kSlab, 1024), kmaj = sdesc_sw128(base, 0, 1024);
+            const uint64_t d_xw = mn + (S::xw >> 4), d_h = mn + (S::h >> 4);
+            auto step_mn = [](int q) { return (uint64_t)(q * 128); };                             // 16 rows of 128 bytes
+            auto step_k = [](int q) { return (uint64_t)((q >> 2) * (kSlab >> 4) + (q & 3) * 2); };   // 32 bytes; the next slab
+            uint32_t nG = 0, mS = 0, nY = 0;     // mS: halves of tiles
             WaitClock clock;
             uint32_t idle = 0;
-            while ((STATE ? nS : nY) < nsteps) {
+            while (STATE ? mS < 2 * nsteps : nY < nsteps) {
                 bool moved = false;
-                // S(n) = B^T (hi + lo): group C has both terms; B has landed
-                if (nS < nsteps && mbar_test(bar(B_XW_READY), nS & 1) &&
-                    mbar_test(bar(B_RING_FULL + slot_b(nS)), use_bc(nS) & 1)) {
+                // S(n), half by half: B^T times the three terms of diag(w) X, smallest first
+                const uint32_t nS = mS >> 1, hf = mS & 1;
+                if (nS < nsteps && mbar_test(bar(B_XW_READY), hf) &&
+                    (hf || mbar_test(bar(B_RING_FULL + slot_b(nS)), use_bc(nS) & 1))) {
                     tc_fence_after();
-                    const uint32_t sB = ring(slot_b(nS));
-#pragma unroll 1
-                    for (int q = 0; q < 2 * kTile / 16; ++q)
-                        mma_bf16_ss(tS(nS), sdesc_sw128(sB + (q & 7) * 2048, kSlab, 1024),
-                                    sdesc_sw128(base + S::xw + q * 2048, kSlab, 1024), id_state, q > 0);
+                    const uint64_t dB = mn + ((S::ring + slot_b(nS) * 2 * kSlab + hf * kHalf) >> 4);
+                    const uint32_t d = tS(nS);
+#pragma unroll
+                    for (int t = 2; t >= 0; --t)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mma_bf16_ss(d, dB + step_mn(q), d_xw + t * (kHalf >> 4) + step_mn(q), id_state,
+                                        t == 2 && q == 0 ? hf : 1u);
                     mma_commit(bar(B_S_READY));
                     // B goes free with the second of its two readers, S and G
-                    if (STATE || nG > nS) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
-                    ++nS;
+                    if (hf && (STATE || nG > nS)) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
+                    ++mS;
                     moved = true;
                 }
                 if (!STATE) {
-                    // Y(n) = M X and Yo(n) = C H
-                    if (nY < nS && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1)) {
+                    // Y(n) = M X and Yo(n) = C H, once both halves of diag(w) X are built (what is
+                    // behind the sequence's end in x is zero then)
+                    if (2 * nY + 1 < mS && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1)) {
                         tc_fence_after();
-                        const uint32_t sX = base + xslot(nY), sC = ring(slot_c(nY));
-#pragma unroll 1
-                        for (int q = 0; q < kTile / 16; ++q)
-                            mma_bf16_ts(tY(nY), tG(nY) + 8 * q, sdesc_sw128(sX + q * 2048, kSlab, 1024), id_o, q > 0);
-                        if (!w.zero_start()) {
-#pragma unroll 1
+                        const uint64_t dX = mn + (xslot(nY) >> 4), dC = kmaj + ((S::ring + slot_c(nY) * 2 * kSlab) >> 4);
+                        const uint32_t dy = tY(nY), dm = tG(nY);
+#pragma unroll
+                        for (int q = 0; q < kTile / 16; ++q) mma_bf16_ts(dy, dm + 8 * q, dX + step_mn(q), id_o, q > 0);
+                        if (!(sm.info[nY % kVec].flags & kZeroStart)) {
+#pragma unroll
                             for (int q = 0; q < N / 16; ++q)
-                                mma_bf16_ss(tG(nY) + 64, sdesc_sw128(sC + (q >> 2) * kSlab + (q & 3) * 32, 0, 1024),
-                                            sdesc_sw128(base + S::h + q * 2048, kSlab, 1024), id_o, q > 0);
+                                mma_bf16_ss(dm + 64, dC + step_k(q), d_h + step_mn(q), id_o, q > 0);
                         }
                         mma_commit(bar(B_Y_READY + (nY & 1)));
                         mma_commit(bar(B_RING_EMPTY + slot_c(nY)));
                         ++nY;
-                        w.tile();
                         moved = true;
                     }
                     // G(n) = C B^T: the operands have landed and tile n - 2's buffers are read
@@ -473,14 +484,13 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                         mbar_test(bar(B_RING_FULL + slot_b(nG)), use_bc(nG) & 1) &&
                         (nG < 2 || mbar_test(bar(B_G_FREE + (nG & 1)), ((nG >> 1) - 1) & 1))) {
                         tc_fence_after();
-                        const uint32_t sC = ring(slot_c(nG)), sB = ring(slot_b(nG));
-#pragma unroll 1
-                        for (int q = 0; q < N / 16; ++q) {
-                            const uint32_t ko = (q >> 2) * kSlab + (q & 3) * 32;
-                            mma_bf16_ss(tG(nG), sdesc_sw128(sC + ko, 0, 1024), sdesc_sw128(sB + ko, 0, 1024), id_g, q > 0);
-                        }
+                        const uint64_t dC = kmaj + ((S::ring + slot_c(nG) * 2 * kSlab) >> 4);
+                        const uint64_t dB = kmaj + ((S::ring + slot_b(nG) * 2 * kSlab) >> 4);
+                        const uint32_t d = tG(nG);
+#pragma unroll
+                        for (int q = 0; q < N / 16; ++q) mma_bf16_ss(d, dC + step_k(q), dB + step_k(q), id_g, q > 0);
                         mma_commit(bar(B_G_READY + (nG & 1)));
-                        if (nS > nG) mma_commit(bar(B_RING_EMPTY + slot_b(nG)));
+                        if (mS > 2 * nG + 1) mma_commit(bar(B_RING_EMPTY + slot_b(nG)));
                         ++nG;
                         moved = true;
                     }
@@ -501,197 +511,252 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mma_commit(bar(B_DONE));
             mbar_drain(bar(B_DONE), 0);
         }
-    } else if (warp < 6) {
-        // ------------------------------------------------------------ group C
-        const int row = ((warp & 3) << 5) | lane;
-        const uint32_t lane_off = (uint32_t)((warp & 3) << 5) << 16;
-        float H[64];
-        uint32_t raw = 0;
-        auto load_dt = [&](const Walk &w, bool there) {
-            raw = 0;
-            const int t = w.k * kTile + row;
-            if (there && t < w.len) {
-                const __nv_bfloat16 *q = p.dt + (long long)w.b * p.dt_sb + (long long)t * p.dt_st + w.hu() / p.halves;
-                asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(raw) : "l"(q));
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ decays of the coming tiles
+        // (lane l: tokens 4 l .. 4 l + 3 of the tile)
+        Walk w(p, sm.stages);
+        uint32_t raw[4] = {0u, 0u, 0u, 0u};
+        float A = 0.f, D = 0.f, bias = 0.f;
+        auto load = [&](bool there) {
+            if (there && w.first) {
+                A = p.A[w.h];
+                D = !STATE && p.D ? p.D[w.h] : 0.f;
+                bias = p.step.bias ? p.step.bias[w.h] : 0.f;
             }
-        };
-        // the state behind a stage's unit, to the unit's end state or to the cut
-        auto sink = [&](int u, int b, bool to_cut, float decay) {
-            if (to_cut && p.order == kOrderNatural) return;      // the chain has put it there
-            if (row < N && !*abort_flag) {
-                float *d = nullptr;
-                if (to_cut) d = p.cut + (size_t)blockIdx.x * 64 * N;
-                else if (p.state_out) d = p.state_out + ((size_t)(p.rows ? p.rows[b] : b) * p.HU + u % p.HU) * 64 * N;
-                if (d) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) d[(size_t)j * N + row] = H[j];
-                }
-            }
-            if (to_cut) {
-                sync_c();
-                if (row == 0) {
-                    if (STATE) p.cut_decay[blockIdx.x] = decay;
-                    else if (p.order == kOrderHandoff && !*abort_flag) flag_release(p.flags + blockIdx.x, 1u);
+            for (int i = 0; i < 4; ++i) {
+                const int t = w.k * kTile + 4 * lane + i;
+                raw[i] = 0;
+                if (there && t < w.len) {
+                    const __nv_bfloat16 *q = p.dt + (long long)w.b * p.dt_sb + (long long)t * p.dt_st + w.h;
+                    asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(raw[i]) : "l"(q));
                 }
             }
         };
-        Walk w(p, sm.stages), ahead(p, sm.stages);
         bool go = w.unit();
-        bool more = ahead.unit();
-        load_dt(ahead, more);
+        load(go);
         uint32_t n = 0;
-        float gprev = 0.f, gall = 1.f;       // exp(A * sum of dt) of the previous tile, of the stage so far
-        int pu = 0, pb = 0;
-        bool pend = false, pcut = false;     // the previous tile ended its unit or stage
-        // H <- exp(A sum dt) H + S of tile m
-        auto advance = [&](uint32_t m) {
-            tc_fence_after();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t sv[32];
-                tmem_ld32(tS(m) + lane_off + half * 32, sv);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) H[half * 32 + j] = fmaf(gprev, H[half * 32 + j], __uint_as_float(sv[j]));
-            }
-            tc_fence_before();
-        };
-        // an aborted CTA walks on to its end (its waits return at once): a group's
-        // threads never part ways ahead of their barriers
 #pragma unroll 1
-        for (; go; go = w.tile(), ++n) {
-            const int valid = w.len - w.k * kTile;       // rows of the tile that hold tokens
-            const int h = w.hu() / p.halves;
-            const float A = p.A[h];
-            const float v = row < valid ? p.step(bf2f(raw), h) : 0.f;
-            if (more) more = ahead.tile();
-            load_dt(ahead, more);
-            // sums of dt up to and with the row, and behind it
-            float pf = v, sf = v;
+        for (; go; ++n) {
+            const int b = w.b, h = w.h, hu = w.hu, t0 = w.k * kTile, len = w.len;
+            const Stage &st = sm.stages[w.s];
+            const bool zero = w.first && !st.from_cut && (STATE || p.init == nullptr);
+            int flags = (zero ? kZeroStart : 0) | (w.first ? kFirst : 0) | (w.k + 1 == w.k1 ? kLast : 0) |
+                        (st.from_cut ? kFromCut : 0) | (st.to_cut ? kToCut : 0);
+            const float A_ = A, D_ = D;
+            float v[4], up[4], down[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = t0 + 4 * lane + i < len ? p.step.with(bf2f(raw[i]), bias) : 0.f;
+            go = w.tile();
+            load(go);            // the next tile's step sizes are on their way meanwhile
+            up[0] = v[0];
+            down[3] = 0.f;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) up[i] = up[i - 1] + v[i];
+#pragma unroll
+            for (int i = 2; i >= 0; --i) down[i] = down[i + 1] + v[i + 1];
+            const float mine = up[3];
+            float pre = mine, suf = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float up = __shfl_up_sync(0xffffffffu, pf, o), dn = __shfl_down_sync(0xffffffffu, sf, o);
-                if (lane >= o) pf += up;
-                if (lane + o < 32) sf += dn;
+                const float x = __shfl_up_sync(0xffffffffu, pre, o), y = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane >= o) pre += x;
+                if (lane + o < 32) suf += y;
             }
-            float *red = sm.red[n & 1];
-            if (lane == 31) red[row >> 5] = pf;
-            sync_c();
-            float ahead_sum = 0.f, behind = 0.f, tot = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (q < (row >> 5)) ahead_sum += red[q];
-                if (q > (row >> 5)) behind += red[q];
-            }
-            tot = (red[0] + red[1]) + (red[2] + red[3]);
+            const float all = A_ * __shfl_sync(0xffffffffu, pre, 31);
             // a row's weight in the state: the sum behind it, added up from the end
-            const float weight = expf(A * ((sf - v) + behind)) * v;
-            if (!STATE) {
-                const float my_a = A * (ahead_sum + pf);
-                const uint32_t vb = n & 1;
-                if (n >= 2) mbar_wait_ool(bar(B_VEC_FREE + vb), ((n >> 1) - 1) & 1, abort_flag, p.status, 920);
-                TileVec &V = sm.vec[vb];
-                V.a[row] = my_a;
-                V.dt[row] = v;
-                V.col[row] = __expf(0.5f * A * tot - my_a) * v;
-                sync_c();
-                if (row == 0) mbar_arrive(bar(B_VEC_READY + vb));
+            const float ahead = __shfl_up_sync(0xffffffffu, pre, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
+            const bool one = all > -kMaxSpan;
+            if (one) flags |= kOneFactor;
+            float a4[4], c4[4], w4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a4[i] = A_ * ((lane ? ahead : 0.f) + up[i]);
+                c4[i] = one ? __expf(0.5f * all - a4[i]) * v[i] : v[i];
+                w4[i] = expf(A_ * ((lane < 31 ? behind : 0.f) + down[i])) * v[i];
             }
-            // diag(w) X in two terms, once S of the tile before has read its buffers
-            mbar_wait_ool(bar(B_X_FULL + slot_x(n)), use_x(n) & 1, abort_flag, p.status, 921);
-            if (n >= 1) mbar_wait_ool(bar(B_S_READY), (n - 1) & 1, abort_flag, p.status, 922);
-            uint8_t *xt = g + xslot(n);
-            if (row < valid) {
-                split_row(xt, g + S::xw, g + S::xw + kSlab, row, weight);
-            } else {
-                // what lies behind the sequence may be anything: zero it wherever a product
-                // sums over it (x, diag(w) X, B)
-                zero_row(g + S::xw, row);
-                zero_row(g + S::xw + kSlab, row);
-                zero_row(xt, row);
-                mbar_wait_ool(bar(B_RING_FULL + slot_b(n)), use_bc(n) & 1, abort_flag, p.status, 923);
-                for (int sl = 0; sl < NSLAB; ++sl) zero_row(g + S::ring + slot_b(n) * 2 * kSlab + sl * kSlab, row);
+            const uint32_t vb = n % kVec;
+            if (n >= kVec) mbar_wait_ool(bar(B_VEC_FREE + vb), ((n / kVec) - 1) & 1, abort_flag, p.status, 920);
+            TileInfo &I = sm.info[vb];
+            reinterpret_cast<float4 *>(I.a)[lane] = make_float4(a4[0], a4[1], a4[2], a4[3]);
+            reinterpret_cast<float4 *>(I.col)[lane] = make_float4(c4[0], c4[1], c4[2], c4[3]);
+            reinterpret_cast<float4 *>(I.w)[lane] = make_float4(w4[0], w4[1], w4[2], w4[3]);
+            if (lane == 0) {
+                I.b = b; I.h = h; I.hu = hu; I.t0 = t0; I.len = len; I.flags = flags;
+                I.decay = expf(all);
+                I.D = D_;
             }
-            fence_proxy_async_smem();
-            sync_c();
-            if (row == 0) {
-                mbar_arrive(bar(B_XW_READY));
-                if (STATE) mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_VEC_READY + vb));
+        }
+    } else if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------ group C
+        const int row = ((warp & 3) << 5) | lane;                 // row n of the state
+        const int ph = warp >= 8;                                 // its columns [32 ph, 32 ph + 32)
+        const uint32_t lane_off = ((uint32_t)((warp & 3) << 5) << 16) + 32 * ph;
+        const int cid = tid - 128, br = cid >> 2, bq = cid & 3;   // diag(w) X: row br of the half tile, 16 columns
+        float H[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) H[j] = 0.f;
+        float decay = 0.f, all = 1.f;     // of the previous tile; of the part so far
+        int pb = 0, phu = 0, pflags = 0;  // of the previous tile
+        // an aborted CTA walks on to its end (its waits return at once): a group's
+        // threads never part ways ahead of their barriers. The step behind the last
+        // tile only takes its state.
+#pragma unroll 1
+        for (uint32_t n = 0; n <= nsteps; ++n) {
+            const TileInfo &I = sm.info[n % kVec];
+            const bool tile = n < nsteps;
+            int t0 = 0, len = 0;
+            if (tile) {
+                mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 921);
+                mbar_wait_ool(bar(B_X_FULL + slot_x(n)), use_x(n) & 1, abort_flag, p.status, 922);
+                t0 = I.t0;
+                len = I.len;
             }
-            // the state entering the tile
-            if (n >= 1) advance(n - 1);
-            if (pend) sink(pu, pb, pcut, gall);
-            if (w.first) {
-                gall = 1.f;
+            // half of diag(w) X in three terms
+            auto build = [&](int hf) {
+                const int r = hf * 64 + br;
+                uint8_t *xt = g + xslot(n) + r * 128;
+                uint8_t *dst = g + S::xw + br * 128;
+                if (t0 + r < len) {
+                    const float wt = I.w[r];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int at = ((2 * bq + c) ^ (r & 7)) << 4;
+                        uint4 t[3];
+                        split3(*reinterpret_cast<const uint4 *>(xt + at), wt, t);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(dst + k * kHalf + at) = t[k];
+                    }
+                } else {
+                    // what lies behind the sequence may be anything: zero it wherever a product
+                    // sums over it (x, diag(w) X, B)
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 2; ++c) {
+                        const int at = ((2 * bq + c) ^ (r & 7)) << 4;
+                        *reinterpret_cast<uint4 *>(xt + at) = z;
+                        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(dst + k * kHalf + at) = z;
+                    }
+                    mbar_wait_ool(bar(B_RING_FULL + slot_b(n)), use_bc(n) & 1, abort_flag, p.status, 923);
+                    uint4 *bt = reinterpret_cast<uint4 *>(g + S::ring + slot_b(n) * 2 * kSlab + r * 128);
+                    for (int c = 0; c < 2 * NSLAB; ++c) bt[(c >> 1) * (kSlab / 16) + 2 * bq + (c & 1)] = z;
+                }
+                fence_proxy_async_smem();
+                sync_state();
+                if (cid == 0) mbar_arrive(bar(B_XW_READY));
+            };
+            // S of the tile before has read its terms (and is complete)
+            if (n >= 1) mbar_wait_ool(bar(B_S_READY), 1, abort_flag, p.status, 924);
+            if (tile) build(0);
+            // H <- exp(a_T) H + S of the tile before
+            if (n >= 1) {
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t sv[16];
+                    tmem_ld16(tS(n - 1) + lane_off + q * 16, sv);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) H[q * 16 + j] = fmaf(decay, H[q * 16 + j], __uint_as_float(sv[j]));
+                }
+                tc_fence_before();
+                if (pflags & kLast) {
+                    // the state behind the unit or the part of it: the end state, or to the CTA
+                    // behind (with kOrderNatural the chain has put it there)
+                    const bool cut = pflags & kToCut;
+                    float *d = nullptr;
+                    if (!cut) {
+                        if (p.state_out) d = p.state_out + ((size_t)(p.rows ? p.rows[pb] : pb) * p.HU + phu) * 64 * N;
+                    } else if (p.order != kOrderNatural) {
+                        d = p.cut + (size_t)blockIdx.x * 64 * N;
+                    }
+                    if (d && row < N && !*abort_flag) {
+                        d += 32 * ph * N + row;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) d[j * N] = H[j];
+                    }
+                    if (cut && p.order != kOrderNatural) {
+                        sync_state();
+                        if (cid == 0) {
+                            if (STATE) p.cut_decay[blockIdx.x] = all;
+                            else if (!*abort_flag) flag_release(p.flags + blockIdx.x, 1u);
+                        }
+                    }
+                }
+            }
+            if (!tile) break;
+            const int flags = I.flags;
+            if (flags & kFirst) {
+                all = 1.f;
                 const float *from = nullptr;
                 if (!STATE) {
-                    if (w.st[w.s].from_cut) {
+                    if (flags & kFromCut) {
                         from = p.cut + (size_t)(blockIdx.x - 1) * 64 * N;
                         if (p.order == kOrderHandoff) {
-                            if (row == 0) flag_wait(p.flags + blockIdx.x - 1, 1u, abort_flag, p.status, 924);
-                            sync_c();
+                            if (cid == 0) flag_wait(p.flags + blockIdx.x - 1, 1u, abort_flag, p.status, 925);
+                            sync_state();
                         }
-                    } else if (p.init && p.order == kOrderNatural && w.st[w.s].to_cut) {
+                    } else if (p.init && p.order == kOrderNatural && (flags & kToCut)) {
                         from = p.start + (size_t)blockIdx.x * 64 * N;
                     } else if (p.init) {
-                        from = p.init + ((size_t)(p.rows ? p.rows[w.b] : w.b) * p.HU + w.hu()) * 64 * N;
+                        from = p.init + ((size_t)(p.rows ? p.rows[I.b] : I.b) * p.HU + I.hu) * 64 * N;
                     }
                 }
                 if (from && row < N) {
                     // another CTA of this launch may have written it: past L1
+                    from += 32 * ph * N + row;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) H[j] = __ldcg(from + (size_t)j * N + row);
+                    for (int j = 0; j < 32; ++j) H[j] = __ldcg(from + j * N);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) H[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) H[j] = 0.f;
                 }
             }
             if (!STATE) {
                 // C H of the tile before has read the buffer
-                if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 925);
-                if (row < N && !w.zero_start()) {
+                if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
+                if (row < N && !(flags & kZeroStart)) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, c)) =
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, 4 * ph + c)) =
                             make_uint4(pack_bf16x2(H[8 * c], H[8 * c + 1]), pack_bf16x2(H[8 * c + 2], H[8 * c + 3]),
                                        pack_bf16x2(H[8 * c + 4], H[8 * c + 5]), pack_bf16x2(H[8 * c + 6], H[8 * c + 7]));
                 }
                 fence_proxy_async_smem();
-                sync_c();
-                if (row == 0) mbar_arrive(bar(B_H_READY));
+                tc_fence_before();
+                sync_state();
+                if (cid == 0) mbar_arrive(bar(B_H_READY));
             }
-            gprev = expf(A * tot);
-            gall *= gprev;
-            pend = w.last();
-            pu = w.u;
-            pb = w.b;
-            pcut = w.st[w.s].to_cut;
+            decay = I.decay;
+            all *= decay;
+            pflags = flags;
+            pb = I.b;
+            phu = I.hu;
+            mbar_wait_ool(bar(B_S_READY), 0, abort_flag, p.status, 927);
+            build(1);
+            if (cid == 0) {
+                mbar_arrive(bar(B_VEC_FREE + n % kVec));
+                if (STATE) mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
+            }
         }
-        if (n >= 1) {
-            mbar_wait_ool(bar(B_S_READY), (n - 1) & 1, abort_flag, p.status, 926);
-            advance(n - 1);
-            if (pend) sink(pu, pb, pcut, gall);
-        }
-    } else if (!STATE) {
+    } else if (!STATE && warp >= 12) {
         // ------------------------------------------------------------ groups A and B
-        const bool is_b = warp >= 10;
+        const bool is_b = warp >= 16;
         const int row = ((warp & 3) << 5) | lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) << 5) << 16;
         const int wq = warp & 3;
         auto sync_g = [&]() { if (is_b) sync_b(); else sync_a(); };
-        Walk w(p, sm.stages);
-        bool go = w.unit();
-        if (is_b && go) go = w.tile();
-        uint32_t n = is_b ? 1 : 0;
+        const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
 #pragma unroll 1
-        for (; go; n += 2) {
-            const uint32_t par = (n >> 1) & 1, vb = n & 1;
+        for (uint32_t n = is_b; n < nsteps; n += 2) {
+            const uint32_t par = (n >> 1) & 1, nb = n & 1;
             // ---------------- the mask
-            mbar_wait_ool(bar(B_VEC_READY + vb), par, abort_flag, p.status, 930);
-            const TileVec &V = sm.vec[vb];
-            const float my_a = V.a[row], all = V.a[kTile - 1];
-            const bool one_factor = all > -kMaxSpan;
-            mbar_wait_ool(bar(B_G_READY + vb), par, abort_flag, p.status, 931);
+            mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 930);
+            const TileInfo &I = sm.info[n % kVec];
+            const float my_a = I.a[row], all = I.a[kTile - 1];
+            const bool one = I.flags & kOneFactor;
+            mbar_wait_ool(bar(B_G_READY + nb), par, abort_flag, p.status, 931);
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
 #pragma unroll 1
@@ -705,18 +770,18 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     tmem_ld32(tg + J * 32, gv);
                     tmem_wait_ld();
                     const int s0 = J * 32;
-                    if (one_factor) {
+                    if (one) {
 #pragma unroll
                         for (int q = 0; q < 32; q += 4) {
-                            const float4 c = *reinterpret_cast<const float4 *>(&V.col[s0 + q]);
+                            const float4 c = *reinterpret_cast<const float4 *>(&I.col[s0 + q]);
                             m[q / 2] = scaled_pair(gv[q], gv[q + 1], c.x, c.y);
                             m[q / 2 + 1] = scaled_pair(gv[q + 2], gv[q + 3], c.z, c.w);
                         }
                     } else {
 #pragma unroll
                         for (int q = 0; q < 32; q += 2) {
-                            const float e0 = __expf(fminf(my_a - V.a[s0 + q], 0.f)) * V.dt[s0 + q];
-                            const float e1 = __expf(fminf(my_a - V.a[s0 + q + 1], 0.f)) * V.dt[s0 + q + 1];
+                            const float e0 = __expf(fminf(my_a - I.a[s0 + q], 0.f)) * I.col[s0 + q];
+                            const float e1 = __expf(fminf(my_a - I.a[s0 + q + 1], 0.f)) * I.col[s0 + q + 1];
                             m[q / 2] = scaled_pair(gv[q], gv[q + 1], e0, e1);
                         }
                     }
@@ -733,22 +798,17 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tmem_wait_st();
             tc_fence_before();
             sync_g();
-            if (row == 0) {
-                mbar_arrive(bar(B_M_READY + vb));
-                mbar_arrive(bar(B_VEC_FREE + vb));
-            }
+            if (row == 0) mbar_arrive(bar(B_M_READY + nb));
             // ---------------- the output
-            const int t = w.k * kTile + row;
-            const bool zs = w.zero_start();
-            const float rf = one_factor ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a);
-            const int hu = w.hu();
-            const float D = p.D ? p.D[hu / p.halves] : 0.f;
-            __nv_bfloat16 *dst = p.out + (((size_t)w.b * p.L + t) * p.HU + hu) * 64;
+            const int t = I.t0 + row;
+            const bool zs = I.flags & kZeroStart;
+            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a), D = I.D;
+            __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
+            const bool keep = t < I.len, inside = t < p.L;
             const uint8_t *xt = g + xslot(n);
-            mbar_wait_ool(bar(B_Y_READY + vb), par, abort_flag, p.status, 932);
+            mbar_wait_ool(bar(B_Y_READY + nb), par, abort_flag, p.status, 932);
             tc_fence_after();
-            const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-            const bool store = t < p.L && !*abort_flag, keep = t < w.len;
+            const bool store = inside && !*abort_flag;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t yv[16], ov[16], o8[8];
@@ -776,11 +836,10 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tc_fence_before();
             sync_g();
             if (row == 0) {
-                mbar_arrive(bar(B_G_FREE + vb));
+                mbar_arrive(bar(B_VEC_FREE + n % kVec));
+                mbar_arrive(bar(B_G_FREE + nb));
                 mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
             }
-            go = w.tile();
-            if (go) go = w.tile();
         }
     }
 
@@ -903,7 +962,7 @@ cudaError_t launch_tc(const CUtensorMap &x, const CUtensorMap &b, const CUtensor
     static_assert(Layout<N, STATE>::small + sizeof(Small) + 1024 <= 232448, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k<<<ctas, kThreads, smem, stream>>>(x, b, c, p);
+    k<<<ctas, STATE ? kStateThreads : kThreads, smem, stream>>>(x, b, c, p);
     return cudaGetLastError();
 }
 
