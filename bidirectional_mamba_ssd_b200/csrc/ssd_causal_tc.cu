@@ -37,8 +37,9 @@
 // mask and output of the even and the odd tiles, so that one tile's mask overlaps
 // the other's products and output; thread r owns tile row r.
 // TMEM (512 columns): two of {G 128: M packed over its first half once read, Yo over
-// its second}, two Y, two S. Shared memory: C and B two tiles deep, x two, H once,
-// the three terms of half a tile of diag(w) X.
+// its second}, two Y, S in two parts (the first term of diag(w) X and the other two:
+// an MMA with N = 128 reads B^T once for two terms). Shared memory: C and B two tiles
+// deep, x three, H once, the three terms of half a tile of diag(w) X.
 // Every wait is bounded; one that expires sets the workspace's timeout flag and
 // the CTA runs to its end without storing.
 #include <cuda.h>
@@ -59,7 +60,7 @@ using namespace fused;
 constexpr int kTile = 128;
 constexpr uint32_t kSlab = 16384;     // 128 rows x 128 bytes
 constexpr int kThreads = 640;
-constexpr int kStateThreads = 384;    // without groups A and B
+constexpr int kStateThreads = 384;    // without the output groups
 constexpr int kVec = 4;               // tiles whose decays are kept
 constexpr uint32_t kHalf = 8192;      // 64 rows x 128 bytes
 constexpr float kMaxSpan = 120.f;     // decay of a tile up to which its mask is one factor per column
@@ -208,8 +209,10 @@ struct Walk {
     int b = 0, hu = 0, h = 0, len = 0, k = 0, k1 = 0;
     bool first = false;            // the tile is the first of its unit's here
     __device__ __forceinline__ Walk(const TcParams &p_, const Stage *st_) : p(p_), st(st_) {}
-    // the next unit with tiles; false behind the last
-    __device__ __forceinline__ bool unit() {
+    // the next tile; false behind the last (one call site a role keeps the code small)
+    __device__ __forceinline__ bool next() {
+        first = false;
+        if (++k < k1) return true;
         while (true) {
             ++j;
             while (s < 3 && j >= st[s].n) {
@@ -234,16 +237,11 @@ struct Walk {
             return true;
         }
     }
-    // the next tile
-    __device__ __forceinline__ bool tile() {
-        first = false;
-        return ++k < k1 ? true : unit();
-    }
 };
 
 template <int N, bool STATE>
 struct Layout {
-    static constexpr int kX = STATE ? 3 : 2;               // x slots
+    static constexpr int kX = 3;                           // x slots
     static constexpr uint32_t kBC = N * 256;               // bytes of a B or C tile
     static constexpr uint32_t ring = 0;                    // 4 slots of 32 KB
     static constexpr uint32_t x0 = 4 * 2 * kSlab;
@@ -254,12 +252,12 @@ struct Layout {
 
 enum {
     B_RING_FULL = 0, B_RING_EMPTY = 4, B_X_FULL = 8, B_X_EMPTY = 12,
-    B_G_READY = 16,      // 2: MMA -> group: G of the tile
-    B_M_READY = 18,      // 2: group -> MMA: M of the tile
-    B_Y_READY = 20,      // 2: MMA -> group (and C): Y and Yo of the tile
-    B_G_FREE = 22,       // 2: group -> MMA: the tile's TMEM buffers are read
-    B_VEC_READY = 24,    // kVec: warp 2 -> groups
-    B_VEC_FREE = 28,     // kVec: C and the tile's group -> warp 2
+    B_G_READY = 16,      // 2: MMA -> output groups: G of the tile
+    B_M_READY = 18,      // 2: output groups -> MMA: M of the tile
+    B_Y_READY = 20,      // 2: MMA -> output groups and C: Y and Yo of the tile
+    B_G_FREE = 22,       // 2: output groups -> MMA: the tile's TMEM buffers are read
+    B_VEC_READY = 24,    // kVec: warp 2 -> C and the output groups
+    B_VEC_FREE = 28,     // kVec: C and the output groups -> warp 2
     B_XW_READY = 32,     // C -> MMA, twice a tile
     B_S_READY,           // MMA -> C, twice a tile
     B_H_READY,           // C -> MMA
@@ -270,7 +268,7 @@ enum {
 // What is known of a tile, from warp 2 to the other warps: a_s, the column
 // factors of M (the step sizes where each entry takes its own exponential), the
 // weights in the state.
-enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32 };
+enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64 };
 struct TileInfo {
     float a[kTile], col[kTile], w[kTile];
     int b, h, hu, t0, len, flags;
@@ -285,7 +283,6 @@ struct Small {
     int pad;
     Stage stages[3];
     alignas(16) TileInfo info[kVec];
-    long long scratch[kThreads + 8];
 };
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -298,6 +295,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// 8 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
 }
 
 typedef unsigned long long pair_t;
@@ -353,13 +363,14 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     uint8_t *g = smem_raw + (base - smem_u32(smem_raw));
     Small &sm = *reinterpret_cast<Small *>(g + S::small);
     volatile int *abort_flag = &sm.abort_flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's index as the compiler can see it to be: one value for all its lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
 
     if (tid == 0) {
         sm.abort_flag = 0;
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(bar(i), !STATE && i >= B_VEC_FREE && i < B_VEC_FREE + kVec ? 2 : 1);
+            mbar_init(bar(i), !STATE && ((i >= B_VEC_FREE && i < B_VEC_FREE + kVec) || (i >= B_X_EMPTY && i < B_X_EMPTY + kX)) ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -367,7 +378,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         tmem_relinquish();
     }
     grid_dependency_wait();
-    make_stages(p, blockIdx.x, gridDim.x, sm.stages, &sm.nsteps, sm.scratch);
+    // (the ring is not in use yet)
+    make_stages(p, blockIdx.x, gridDim.x, sm.stages, &sm.nsteps, reinterpret_cast<long long *>(g));
     if (STATE && tid == 0) {
         const Stage r = sm.stages[2];
         p.link[blockIdx.x] = r.n ? make_int2(r.k0 ? kLinkNext : kLinkFirst, r.u0) : make_int2(kLinkNone, 0);
@@ -375,30 +387,34 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    const uint32_t nsteps = (uint32_t)sm.nsteps;
-    auto tG = [&](uint32_t n) { return tmem + 128 * (n & 1); };          // G, then M in [0, 64) and Yo in [64, 128)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+    const uint32_t nsteps = __shfl_sync(0xffffffffu, (uint32_t)sm.nsteps, 0);
+    auto tG = [&](uint32_t n) { return tmem + 128 * (n & 1); };
     auto tY = [&](uint32_t n) { return tmem + 256 + 64 * (n & 1); };
-    auto tS = [&](uint32_t n) { return tmem + 384 + 64 * (n & 1); };
+    const uint32_t tS = tmem + 384;
     // ring slots and their use counts
     auto slot_c = [](uint32_t n) { return (2 * n) & 3; };
     auto slot_b = [](uint32_t n) { return STATE ? n & 3 : (2 * n + 1) & 3; };
     auto use_bc = [](uint32_t n) { return STATE ? n >> 2 : n >> 1; };
-    auto slot_x = [](uint32_t n) { return n % kX; };
-    auto use_x = [](uint32_t n) { return n / kX; };
+    auto slot_x = [](uint32_t n) { return n % (uint32_t)kX; };
+    auto use_x = [](uint32_t n) { return n / (uint32_t)kX; };
     auto ring = [&](uint32_t s) { return base + S::ring + s * 2 * kSlab; };
     auto xslot = [&](uint32_t n) { return S::x0 + slot_x(n) * kSlab; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tmap(&tm_x);
             prefetch_tmap(&tm_b);
             if (!STATE) prefetch_tmap(&tm_c);
             Walk w(p, sm.stages);
             uint32_t n = 0;
-            for (bool go = w.unit(); go && !*abort_flag; go = w.tile(), ++n) {
+            for (; w.next() && !*abort_flag; ++n) {
                 const int grp = w.h / p.heads_per_group, t0 = w.k * kTile;
+                const uint32_t xs = slot_x(n);
+                if (use_x(n) >= 1 && !mbar_wait_ool(bar(B_X_EMPTY + xs), (use_x(n) - 1) & 1, abort_flag, p.status, 903)) break;
+                mbar_arrive_expect_tx(bar(B_X_FULL + xs), kSlab);
+                tma_load_4d(base + xslot(n), &tm_x, bar(B_X_FULL + xs), 0, w.hu, t0, w.b);
                 if (!STATE) {
                     const uint32_t s = slot_c(n);
                     if (n >= 2 && !mbar_wait_ool(bar(B_RING_EMPTY + s), (use_bc(n) - 1) & 1, abort_flag, p.status, 901)) break;
@@ -411,10 +427,6 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 mbar_arrive_expect_tx(bar(B_RING_FULL + s), S::kBC);
                 for (int sl = 0; sl < NSLAB; ++sl)
                     tma_load_4d(ring(s) + sl * kSlab, &tm_b, bar(B_RING_FULL + s), 64 * sl, grp, t0, w.b);
-                const uint32_t xs = slot_x(n);
-                if (use_x(n) >= 1 && !mbar_wait_ool(bar(B_X_EMPTY + xs), (use_x(n) - 1) & 1, abort_flag, p.status, 903)) break;
-                mbar_arrive_expect_tx(bar(B_X_FULL + xs), kSlab);
-                tma_load_4d(base + xslot(n), &tm_x, bar(B_X_FULL + xs), 0, w.hu, t0, w.b);
             }
             // every load issued has landed before the CTA may exit: the last use of each slot
             constexpr uint32_t kDeep = STATE ? 4 : 2;
@@ -426,47 +438,46 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_state = idesc_bf16_f32(128, 64, true, true);   // B^T (MN) x diag(w) X (MN)
+        if (elect_one()) {
+            constexpr uint32_t id_s1 = idesc_bf16_f32(128, 64, true, true);      // B^T (MN) x one term of diag(w) X (MN)
+            constexpr uint32_t id_s2 = idesc_bf16_f32(128, 128, true, true);     // B^T (MN) x two terms
             constexpr uint32_t id_g = idesc_bf16_f32(128, 128, false, false);    // C (K) x B (K)
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);      // C (K) x H (MN); M (K) x X (MN)
             // descriptors of the fixed buffers and of ring and x slot 0: another slot,
             // and a K step, only add to the start address (in 16-byte units)
             const uint64_t mn = sdesc_sw128(base, kSlab, 1024), kmaj = sdesc_sw128(base, 0, 1024);
-            const uint64_t d_xw = mn + (S::xw >> 4), d_h = mn + (S::h >> 4);
+            const uint64_t d_xw = sdesc_sw128(base + S::xw, kHalf, 1024), d_h = mn + (S::h >> 4);
             auto step_mn = [](int q) { return (uint64_t)(q * 128); };                             // 16 rows of 128 bytes
             auto step_k = [](int q) { return (uint64_t)((q >> 2) * (kSlab >> 4) + (q & 3) * 2); };   // 32 bytes; the next slab
             uint32_t nG = 0, mS = 0, nY = 0;     // mS: halves of tiles
             WaitClock clock;
             uint32_t idle = 0;
-            while (STATE ? mS < 2 * nsteps : nY < nsteps) {
+            while (mS < 2 * nsteps || (!STATE && nY < nsteps)) {
                 bool moved = false;
-                // S(n), half by half: B^T times the three terms of diag(w) X, smallest first
+                // S(n), half by half: B^T times the three terms of diag(w) X
                 const uint32_t nS = mS >> 1, hf = mS & 1;
                 if (nS < nsteps && mbar_test(bar(B_XW_READY), hf) &&
                     (hf || mbar_test(bar(B_RING_FULL + slot_b(nS)), use_bc(nS) & 1))) {
                     tc_fence_after();
                     const uint64_t dB = mn + ((S::ring + slot_b(nS) * 2 * kSlab + hf * kHalf) >> 4);
-                    const uint32_t d = tS(nS);
 #pragma unroll
-                    for (int t = 2; t >= 0; --t)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma_bf16_ss(d, dB + step_mn(q), d_xw + t * (kHalf >> 4) + step_mn(q), id_state,
-                                        t == 2 && q == 0 ? hf : 1u);
+                    for (int q = 0; q < 4; ++q) {
+                        mma_bf16_ss(tS, dB + step_mn(q), d_xw + step_mn(q), id_s2, q ? 1u : hf);
+                        mma_bf16_ss(tS + 64, dB + step_mn(q), d_xw + 2 * (kHalf >> 4) + step_mn(q), id_s1, 1u);
+                    }
                     mma_commit(bar(B_S_READY));
                     // B goes free with the second of its two readers, S and G
                     if (hf && (STATE || nG > nS)) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
                     ++mS;
                     moved = true;
-                }
-                if (!STATE) {
-                    // Y(n) = M X and Yo(n) = C H, once both halves of diag(w) X are built (what is
-                    // behind the sequence's end in x is zero then)
-                    if (2 * nY + 1 < mS && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1)) {
+                } else if (!STATE) {
+                    // Y(n) = M X and Yo(n) = C H; where the sequence ends in the tile, once group C
+                    // has zeroed what is behind it in x
+                    if (nY < nG && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1) &&
+                        (2 * nY + 1 < mS || !(sm.info[nY % kVec].flags & kPartial))) {
                         tc_fence_after();
                         const uint64_t dX = mn + (xslot(nY) >> 4), dC = kmaj + ((S::ring + slot_c(nY) * 2 * kSlab) >> 4);
-                        const uint32_t dy = tY(nY), dm = tG(nY);
+                        const uint32_t dm = tG(nY), dy = tY(nY);
 #pragma unroll
                         for (int q = 0; q < kTile / 16; ++q) mma_bf16_ts(dy, dm + 8 * q, dX + step_mn(q), id_o, q > 0);
                         if (!(sm.info[nY % kVec].flags & kZeroStart)) {
@@ -478,7 +489,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                         mma_commit(bar(B_RING_EMPTY + slot_c(nY)));
                         ++nY;
                         moved = true;
-                    }
+                    } else
                     // G(n) = C B^T: the operands have landed and tile n - 2's buffers are read
                     if (nG < nsteps && mbar_test(bar(B_RING_FULL + slot_c(nG)), use_bc(nG) & 1) &&
                         mbar_test(bar(B_RING_FULL + slot_b(nG)), use_bc(nG) & 1) &&
@@ -533,22 +544,33 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 }
             }
         };
-        bool go = w.unit();
-        load(go);
-        uint32_t n = 0;
+        int b = 0, h = 0, hu = 0, t0 = 0, len = 0, flags = 0;     // the tile whose step sizes have been asked for
+        float A_ = 0.f, D_ = 0.f, bias_ = 0.f;
+        bool there = false;
 #pragma unroll 1
-        for (; go; ++n) {
-            const int b = w.b, h = w.h, hu = w.hu, t0 = w.k * kTile, len = w.len;
-            const Stage &st = sm.stages[w.s];
-            const bool zero = w.first && !st.from_cut && (STATE || p.init == nullptr);
-            int flags = (zero ? kZeroStart : 0) | (w.first ? kFirst : 0) | (w.k + 1 == w.k1 ? kLast : 0) |
-                        (st.from_cut ? kFromCut : 0) | (st.to_cut ? kToCut : 0);
-            const float A_ = A, D_ = D;
+        for (uint32_t n = 0;;) {
             float v[4], up[4], down[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = t0 + 4 * lane + i < len ? p.step.with(bf2f(raw[i]), bias) : 0.f;
-            go = w.tile();
-            load(go);            // the next tile's step sizes are on their way meanwhile
+            for (int i = 0; i < 4; ++i) v[i] = t0 + 4 * lane + i < len ? p.step.with(bf2f(raw[i]), bias_) : 0.f;
+            const int b0 = b, h0 = h, hu0 = hu, t00 = t0, len0 = len;
+            int flags0 = flags;
+            const float A0 = A_, D0 = D_;
+            const bool had = there;
+            // the next tile's step sizes are on their way meanwhile
+            there = w.next();
+            load(there);
+            if (there) {
+                const Stage &st = sm.stages[w.s];
+                const bool zero = w.first && !st.from_cut && (STATE || p.init == nullptr);
+                b = w.b; h = w.h; hu = w.hu; t0 = w.k * kTile; len = w.len;
+                flags = (zero ? kZeroStart : 0) | (w.first ? kFirst : 0) | (w.k + 1 == w.k1 ? kLast : 0) |
+                        (st.from_cut ? kFromCut : 0) | (st.to_cut ? kToCut : 0) | (t0 + kTile > len ? kPartial : 0);
+                A_ = A; D_ = D; bias_ = bias;
+            }
+            if (!had) {
+                if (!there) break;
+                continue;
+            }
             up[0] = v[0];
             down[3] = 0.f;
 #pragma unroll
@@ -563,17 +585,17 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 if (lane >= o) pre += x;
                 if (lane + o < 32) suf += y;
             }
-            const float all = A_ * __shfl_sync(0xffffffffu, pre, 31);
+            const float all = A0 * __shfl_sync(0xffffffffu, pre, 31);
             // a row's weight in the state: the sum behind it, added up from the end
             const float ahead = __shfl_up_sync(0xffffffffu, pre, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
             const bool one = all > -kMaxSpan;
-            if (one) flags |= kOneFactor;
+            if (one) flags0 |= kOneFactor;
             float a4[4], c4[4], w4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a4[i] = A_ * ((lane ? ahead : 0.f) + up[i]);
+                a4[i] = A0 * ((lane ? ahead : 0.f) + up[i]);
                 c4[i] = one ? __expf(0.5f * all - a4[i]) * v[i] : v[i];
-                w4[i] = expf(A_ * ((lane < 31 ? behind : 0.f) + down[i])) * v[i];
+                w4[i] = expf(A0 * ((lane < 31 ? behind : 0.f) + down[i])) * v[i];
             }
             const uint32_t vb = n % kVec;
             if (n >= kVec) mbar_wait_ool(bar(B_VEC_FREE + vb), ((n / kVec) - 1) & 1, abort_flag, p.status, 920);
@@ -582,12 +604,14 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             reinterpret_cast<float4 *>(I.col)[lane] = make_float4(c4[0], c4[1], c4[2], c4[3]);
             reinterpret_cast<float4 *>(I.w)[lane] = make_float4(w4[0], w4[1], w4[2], w4[3]);
             if (lane == 0) {
-                I.b = b; I.h = h; I.hu = hu; I.t0 = t0; I.len = len; I.flags = flags;
+                I.b = b0; I.h = h0; I.hu = hu0; I.t0 = t00; I.len = len0; I.flags = flags0;
                 I.decay = expf(all);
-                I.D = D_;
+                I.D = D0;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_VEC_READY + vb));
+            ++n;
+            if (!there) break;
         }
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ group C
@@ -646,21 +670,25 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 sync_state();
                 if (cid == 0) mbar_arrive(bar(B_XW_READY));
             };
-            // S of the tile before has read its terms (and is complete)
-            if (n >= 1) mbar_wait_ool(bar(B_S_READY), 1, abort_flag, p.status, 924);
-            if (tile) build(0);
-            // H <- exp(a_T) H + S of the tile before
+            // S of the tile before is complete (and has read its terms):
+            // H <- exp(a_T) H + S
             if (n >= 1) {
+                mbar_wait_ool(bar(B_S_READY), 1, abort_flag, p.status, 924);
                 tc_fence_after();
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t sv[16];
-                    tmem_ld16(tS(n - 1) + lane_off + q * 16, sv);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t sv[2][8];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) tmem_ld8(tS + 64 * k + lane_off + q * 8, sv[k]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) H[q * 16 + j] = fmaf(decay, H[q * 16 + j], __uint_as_float(sv[j]));
+                    for (int j = 0; j < 8; ++j)
+                        H[q * 8 + j] = fmaf(decay, H[q * 8 + j], __uint_as_float(sv[0][j]) + __uint_as_float(sv[1][j]));
                 }
                 tc_fence_before();
+            }
+            if (tile) build(0);
+            if (n >= 1) {
                 if (pflags & kLast) {
                     // the state behind the unit or the part of it: the end state, or to the CTA
                     // behind (with kOrderNatural the chain has put it there)
@@ -737,7 +765,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             build(1);
             if (cid == 0) {
                 mbar_arrive(bar(B_VEC_FREE + n % kVec));
-                if (STATE) mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
+                mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
             }
         }
     } else if (!STATE && warp >= 12) {
@@ -751,7 +779,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll 1
         for (uint32_t n = is_b; n < nsteps; n += 2) {
             const uint32_t par = (n >> 1) & 1, nb = n & 1;
-            // ---------------- the mask
+            // ---------------- the mask: 16 columns at a time, the next ones on their way from
+            // TMEM meanwhile; columns [16 c, 16 c + 16) of M are 8 words over G columns already read
             mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 930);
             const TileInfo &I = sm.info[n % kVec];
             const float my_a = I.a[row], all = I.a[kTile - 1];
@@ -759,41 +788,50 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mbar_wait_ool(bar(B_G_READY + nb), par, abort_flag, p.status, 931);
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
-#pragma unroll 1
-            for (int J = 0; J < 4; ++J) {
-                uint32_t m[16];
-                if (J > wq) {
+            const int chunks = 2 * wq + 2;             // up to and with the diagonal
+            auto mask = [&](int c, const uint32_t (&gv)[16]) {
+                uint32_t m[8];
+                if (one) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) m[q] = 0u;
-                } else {
-                    uint32_t gv[32];
-                    tmem_ld32(tg + J * 32, gv);
-                    tmem_wait_ld();
-                    const int s0 = J * 32;
-                    if (one) {
-#pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            const float4 c = *reinterpret_cast<const float4 *>(&I.col[s0 + q]);
-                            m[q / 2] = scaled_pair(gv[q], gv[q + 1], c.x, c.y);
-                            m[q / 2 + 1] = scaled_pair(gv[q + 2], gv[q + 3], c.z, c.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 32; q += 2) {
-                            const float e0 = __expf(fminf(my_a - I.a[s0 + q], 0.f)) * I.col[s0 + q];
-                            const float e1 = __expf(fminf(my_a - I.a[s0 + q + 1], 0.f)) * I.col[s0 + q + 1];
-                            m[q / 2] = scaled_pair(gv[q], gv[q + 1], e0, e1);
-                        }
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
+                        m[q / 2] = scaled_pair(gv[q], gv[q + 1], f.x, f.y);
+                        m[q / 2 + 1] = scaled_pair(gv[q + 2], gv[q + 3], f.z, f.w);
                     }
-                    if (J == wq) {
-                        // entries behind the row's own token are dropped, never multiplied
+                } else {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            m[q] = 2 * q + 1 <= lane ? m[q] : 2 * q <= lane ? (m[q] & 0xffffu) : 0u;
+                    for (int q = 0; q < 16; q += 2) {
+                        const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * I.col[16 * c + q];
+                        const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * I.col[16 * c + q + 1];
+                        m[q / 2] = scaled_pair(gv[q], gv[q + 1], e0, e1);
                     }
                 }
-                // columns [32 J, 32 J + 32) of M as 16 words over G columns already read
-                tmem_st16(tg + J * 16, m);
+                if (c >= 2 * wq) {
+                    // entries behind the row's own token are dropped, never multiplied
+                    const int own = row - 16 * c;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) m[q] = 2 * q + 1 <= own ? m[q] : 2 * q <= own ? (m[q] & 0xffffu) : 0u;
+                }
+                tmem_st8(tg + 8 * c, m);
+            };
+            uint32_t ga[16], gb[16];
+            tmem_ld16(tg, ga);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int c = 0; c < chunks; c += 2) {
+                tmem_ld16(tg + 16 * c + 16, gb);
+                mask(c, ga);
+                tmem_wait_ld();
+                if (c + 2 < chunks) tmem_ld16(tg + 16 * c + 32, ga);
+                mask(c + 1, gb);
+                tmem_wait_ld();
+            }
+#pragma unroll 1
+            for (int c = chunks; c < 8; c += 2) {
+                uint32_t z[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) z[q] = 0u;
+                tmem_st16(tg + 8 * c, z);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -802,28 +840,23 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // ---------------- the output
             const int t = I.t0 + row;
             const bool zs = I.flags & kZeroStart;
-            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a), D = I.D;
+            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = zs ? 0.f : __expf(my_a), D = I.D;
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
             const bool keep = t < I.len, inside = t < p.L;
             const uint8_t *xt = g + xslot(n);
             mbar_wait_ool(bar(B_Y_READY + nb), par, abort_flag, p.status, 932);
             tc_fence_after();
             const bool store = inside && !*abort_flag;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t yv[16], ov[16], o8[8];
+            auto load = [&](int q, uint32_t (&yv)[16], uint32_t (&ov)[16]) {
                 tmem_ld16(tY(n) + lane_off + q * 16, yv);
-                if (zs) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) ov[c] = 0u;
-                } else {
-                    tmem_ld16(tG(n) + 64 + lane_off + q * 16, ov);
-                }
+                if (!zs) tmem_ld16(tg + 64 + q * 16, ov);
+            };
+            auto emit = [&](int q, const uint32_t (&yv)[16], const uint32_t (&ov)[16]) {
+                uint32_t o8[8];
                 uint4 xv[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) xv[c] = *reinterpret_cast<const uint4 *>(xt + sw128_offset(row, q * 2 + c));
                 const uint32_t *xu = reinterpret_cast<const uint32_t *>(xv);
-                tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const float x0 = __uint_as_float(xu[c] << 16), x1 = __uint_as_float(xu[c] & 0xffff0000u);
@@ -832,6 +865,20 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     o8[c] = keep ? pack_bf16x2(y0, y1) : 0u;
                 }
                 if (store) store32(dst + q * 16, o8, whole);
+            };
+            uint32_t ya[16], oa[16], yb[16], ob[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) oa[c] = ob[c] = 0u;      // stay zero where nothing enters the tile
+            load(0, ya, oa);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+                load(q + 1, yb, ob);
+                emit(q, ya, oa);
+                tmem_wait_ld();
+                if (q == 0) load(2, ya, oa);
+                emit(q + 1, yb, ob);
+                tmem_wait_ld();
             }
             tc_fence_before();
             sync_g();
