@@ -310,16 +310,40 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                  : "r"(taddr));
 }
 
+// Two fp32 values to an instruction.
 typedef unsigned long long pair_t;
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t g0, uint32_t g1, float c0, float c1) {
-    pair_t g, c, m;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(g) : "r"(g0), "r"(g1));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(m) : "l"(g), "l"(c));
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(m));
-    return pack_bf16x2(lo, hi);
+__device__ __forceinline__ pair_t pair_of(uint32_t a, uint32_t b) {
+    pair_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
 }
+__device__ __forceinline__ pair_t pair_of(float a, float b) { return pair_of(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ void halves_of(pair_t v, uint32_t &a, uint32_t &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+    pair_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+    pair_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+    pair_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// the pair rounded to bf16
+__device__ __forceinline__ uint32_t bf16_of(pair_t v) {
+    uint32_t a, b;
+    halves_of(v, a, b);
+    return pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+}
+// two bf16 values as a pair
+__device__ __forceinline__ pair_t wide_of(uint32_t v) { return pair_of(v << 16, v & 0xffff0000u); }
 
 // 32 bytes of one row of the output, in one store where the output is aligned to them.
 __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool whole) {
@@ -333,19 +357,21 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool wh
                  : "memory");
 }
 
-// 16 bytes (8 values) of a row of diag(w) X as three bf16 terms, which carry 24
-// bits of each product.
+// 16 bytes (8 values) of a row of diag(w) X as three bf16 terms. Each takes the
+// upper 8 bits of what is left, cut off rather than rounded, so that together they
+// hold all 24 bits of the fp32 product.
 __device__ __forceinline__ void split3(uint4 x, float w, uint4 (&t)[3]) {
     const uint32_t *q = reinterpret_cast<const uint32_t *>(&x);
+    const pair_t ww = pair_of(w, w), minus = pair_of(-1.f, -1.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float a0 = __uint_as_float(q[j] << 16) * w, a1 = __uint_as_float(q[j] & 0xffff0000u) * w;
+        pair_t a = mul2(wide_of(q[j]), ww);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const uint32_t r = pack_bf16x2(a0, a1);
-            reinterpret_cast<uint32_t *>(&t[k])[j] = r;
-            a0 -= __uint_as_float(r << 16);
-            a1 -= __uint_as_float(r & 0xffff0000u);
+            uint32_t lo, hi;
+            halves_of(a, lo, hi);
+            reinterpret_cast<uint32_t *>(&t[k])[j] = __byte_perm(lo, hi, 0x7632);
+            if (k < 2) a = fma2(pair_of(lo & 0xffff0000u, hi & 0xffff0000u), minus, a);
         }
     }
 }
@@ -619,9 +645,9 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         const int ph = warp >= 8;                                 // its columns [32 ph, 32 ph + 32)
         const uint32_t lane_off = ((uint32_t)((warp & 3) << 5) << 16) + 32 * ph;
         const int cid = tid - 128, br = cid >> 2, bq = cid & 3;   // diag(w) X: row br of the half tile, 16 columns
-        float H[32];
+        pair_t H[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) H[j] = 0.f;
+        for (int j = 0; j < 16; ++j) H[j] = 0ull;
         float decay = 0.f, all = 1.f;     // of the previous tile; of the part so far
         int pb = 0, phu = 0, pflags = 0;  // of the previous tile
         // an aborted CTA walks on to its end (its waits return at once): a group's
@@ -682,8 +708,9 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     for (int k = 0; k < 2; ++k) tmem_ld8(tS + 64 * k + lane_off + q * 8, sv[k]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        H[q * 8 + j] = fmaf(decay, H[q * 8 + j], __uint_as_float(sv[0][j]) + __uint_as_float(sv[1][j]));
+                    for (int j = 0; j < 4; ++j)
+                        H[q * 4 + j] = fma2(pair_of(decay, decay), H[q * 4 + j],
+                                            add2(pair_of(sv[0][2 * j], sv[0][2 * j + 1]), pair_of(sv[1][2 * j], sv[1][2 * j + 1])));
                 }
                 tc_fence_before();
             }
@@ -702,7 +729,12 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     if (d && row < N && !*abort_flag) {
                         d += 32 * ph * N + row;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) d[j * N] = H[j];
+                        for (int j = 0; j < 16; ++j) {
+                            uint32_t v0, v1;
+                            halves_of(H[j], v0, v1);
+                            d[(2 * j) * N] = __uint_as_float(v0);
+                            d[(2 * j + 1) * N] = __uint_as_float(v1);
+                        }
                     }
                     if (cut && p.order != kOrderNatural) {
                         sync_state();
@@ -735,26 +767,11 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     // another CTA of this launch may have written it: past L1
                     from += 32 * ph * N + row;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) H[j] = __ldcg(from + j * N);
+                    for (int j = 0; j < 16; ++j) H[j] = pair_of(__ldcg(from + (2 * j) * N), __ldcg(from + (2 * j + 1) * N));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) H[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) H[j] = 0ull;
                 }
-            }
-            if (!STATE) {
-                // C H of the tile before has read the buffer
-                if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
-                if (row < N && !(flags & kZeroStart)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, 4 * ph + c)) =
-                            make_uint4(pack_bf16x2(H[8 * c], H[8 * c + 1]), pack_bf16x2(H[8 * c + 2], H[8 * c + 3]),
-                                       pack_bf16x2(H[8 * c + 4], H[8 * c + 5]), pack_bf16x2(H[8 * c + 6], H[8 * c + 7]));
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                sync_state();
-                if (cid == 0) mbar_arrive(bar(B_H_READY));
             }
             decay = I.decay;
             all *= decay;
@@ -763,6 +780,20 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             phu = I.hu;
             mbar_wait_ool(bar(B_S_READY), 0, abort_flag, p.status, 927);
             build(1);
+            if (!STATE) {
+                // C H of the tile before has read the buffer
+                if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
+                if (row < N && !(flags & kZeroStart)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, 4 * ph + c)) =
+                            make_uint4(bf16_of(H[4 * c]), bf16_of(H[4 * c + 1]), bf16_of(H[4 * c + 2]), bf16_of(H[4 * c + 3]));
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                sync_state();
+                if (cid == 0) mbar_arrive(bar(B_H_READY));
+            }
             if (cid == 0) {
                 mbar_arrive(bar(B_VEC_FREE + n % kVec));
                 mbar_arrive(bar(B_X_EMPTY + slot_x(n)));
@@ -795,15 +826,15 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
                     for (int q = 0; q < 16; q += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
-                        m[q / 2] = scaled_pair(gv[q], gv[q + 1], f.x, f.y);
-                        m[q / 2 + 1] = scaled_pair(gv[q + 2], gv[q + 3], f.z, f.w);
+                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(f.x, f.y)));
+                        m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), pair_of(f.z, f.w)));
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 16; q += 2) {
                         const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * I.col[16 * c + q];
                         const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * I.col[16 * c + q + 1];
-                        m[q / 2] = scaled_pair(gv[q], gv[q + 1], e0, e1);
+                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(e0, e1)));
                     }
                 }
                 if (c >= 2 * wq) {
@@ -842,7 +873,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const bool zs = I.flags & kZeroStart;
             const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = zs ? 0.f : __expf(my_a), D = I.D;
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
-            const bool keep = t < I.len, inside = t < p.L;
+            const bool keep = t < I.len, inside = t < p.L, partial = I.flags & kPartial;
+            const pair_t rf2 = pair_of(rf, rf), e2 = pair_of(e, e), D2 = pair_of(D, D);
             const uint8_t *xt = g + xslot(n);
             mbar_wait_ool(bar(B_Y_READY + nb), par, abort_flag, p.status, 932);
             tc_fence_after();
@@ -858,11 +890,12 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 for (int c = 0; c < 2; ++c) xv[c] = *reinterpret_cast<const uint4 *>(xt + sw128_offset(row, q * 2 + c));
                 const uint32_t *xu = reinterpret_cast<const uint32_t *>(xv);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float x0 = __uint_as_float(xu[c] << 16), x1 = __uint_as_float(xu[c] & 0xffff0000u);
-                    const float y0 = fmaf(rf, __uint_as_float(yv[2 * c]), fmaf(e, __uint_as_float(ov[2 * c]), D * x0));
-                    const float y1 = fmaf(rf, __uint_as_float(yv[2 * c + 1]), fmaf(e, __uint_as_float(ov[2 * c + 1]), D * x1));
-                    o8[c] = keep ? pack_bf16x2(y0, y1) : 0u;
+                for (int c = 0; c < 8; ++c)
+                    o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]),
+                                         fma2(e2, pair_of(ov[2 * c], ov[2 * c + 1]), mul2(D2, wide_of(xu[c])))));
+                if (partial && !keep) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) o8[c] = 0u;
                 }
                 if (store) store32(dst + q * 16, o8, whole);
             };
