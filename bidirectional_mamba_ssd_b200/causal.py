@@ -11,80 +11,103 @@ their last two dimensions (dt: its last) are contiguous.
 
 Calls without a workspace of their own use the stream's, or, while a CUDA graph
 is being captured, one that belongs to the graph: two graphs never share one.
+
+A single token's kernel takes a few microseconds, so the checks here are written
+to cost little: one pass over each tensor, no objects made on the way.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
-from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _DT, _need, _workspace, lib)
+from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _DT, _workspace, lib)
 
 _INF = float("inf")
+_F32, _I32 = torch.float32, torch.int32
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
-def _rows(t, name, dtype, device, shape):
-    """t has this shape, its dimensions past batch (and token) contiguous."""
+@functools.lru_cache(maxsize=4096)
+def _bytes(device, op, batch, L, H, P, N, G, code):
+    """ssd_workspace_bytes on a device (whose SM count it goes by)."""
+    return lib.ssd_workspace_bytes(op, batch, L, H, P, N, G, 0, code)
+
+
+def _fail(t, name, dtype, dev, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected {dev if dev.type == 'cuda' else 'a CUDA device'}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    raise ValueError(f"{name}: the dimensions past batch and token must be contiguous (shape {tuple(t.shape)}, "
+                     f"strides {t.stride()})")
 
 
-def _inner(t, name, dims):
-    """The last `dims` dimensions of t are contiguous."""
-    st, sh = t.stride(), t.shape
-    if (sh[-1] > 1 and st[-1] != 1) or (dims == 2 and sh[-2] > 1 and st[-2] != sh[-1]):
-        raise ValueError(f"{name}: the last {dims} dimensions must be contiguous (strides {st})")
+def _rows(t, name, dtype, dev, shape, dims):
+    """The strides of t, which has this shape and its last `dims` dimensions contiguous."""
+    try:
+        if t.dtype is dtype and t.device == dev and t.shape == shape:
+            st = t.stride()
+            if (st[-1] == 1 or shape[-1] <= 1) and (dims == 1 or st[-2] == shape[-1] or shape[-2] <= 1):
+                return st
+    except (AttributeError, IndexError):
+        pass
+    _fail(t, name, dtype, dev, shape)
 
 
-def _vector(t, name, dtype, device, n):
+def _whole(t, name, dtype, dev, shape):
+    """The address of t, contiguous and of this shape; 0 for None."""
     if t is None:
         return 0
-    _need(t, name, dtype, device, 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail(t, name, dtype, dev, shape)
 
 
-def _pool(t, name, device, rows, H, P, N):
-    """A pool of states with `rows` pages (None: any number)."""
-    _need(t, name, torch.float32, device, 4)
-    if t.shape[1:] != (H, P, N) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be ({'slots' if rows is None else rows}, {H}, {P}, {N}) (got {tuple(t.shape)})")
+def _lead(t, name, ndim):
+    """Device, I/O type and shape of the tensor that the others are checked against."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {dev})")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims (got {tuple(t.shape)})")
+    return dev, t.dtype, t.shape
+
+
+def _states(t, name, dev, slots, rows, page):
+    """The number of pages of a pool: one a row, or any number where slots name them."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    n = t.shape[0] if slots is not None and t.dim() > 0 else rows
+    _whole(t, name, _F32, dev, (n, *page))
+    return n
 
 
 def _apart(a, b, na, nb):
     """The same array, or no byte in common."""
-    pa, pb = a.data_ptr(), b.data_ptr()
-    if pa != pb and pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size():
+    pa, pb, n = a.data_ptr(), b.data_ptr(), 4 * a.numel()
+    if pa != pb and pa < pb + n and pb < pa + n:
         raise ValueError(f"{na} and {nb} overlap without being the same array")
 
 
-class _On:
-    """The tensors' device as the current one, where it is not already."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _scratch(device, stream, workspace):
+def _scratch(dev, stream, workspace):
     """The workspace of a call: the caller's, the graph's being captured, or the stream's."""
-    if workspace is None and torch.cuda.is_current_stream_capturing():
-        return Workspace(device)
-    if workspace is not None and workspace.device.index not in (None, device.index):
-        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
-    return _workspace(device, stream, workspace)
+    if workspace is None:
+        return Workspace(dev) if _capturing() else _workspace(dev, stream, None)
+    if workspace.device.index not in (None, dev.index):
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    return workspace
 
 
 def ssd_causal_fwd(x, dt, A, B, C, D=None, init=None, *, seqlens=None, slots=None, dt_bias=None, dt_min: float = 0.0,
@@ -98,53 +121,50 @@ def ssd_causal_fwd(x, dt, A, B, C, D=None, init=None, *, seqlens=None, slots=Non
     (nslots, H, P, N) whose page slots[b] is row b's; None starts from zero.
     state_out: where the end states go, laid out as init; with slots it
     defaults to init (in place). dt_bias (H): dt is the raw projection."""
-    _need_cuda(x, "x", 4)
-    dev, io = x.device, x.dtype
-    if io not in _DT:
+    dev, io, xshape = _lead(x, "x", 4)
+    if dev.index != _device():
+        with torch.cuda.device(dev):
+            return ssd_causal_fwd(x, dt, A, B, C, D, init, seqlens=seqlens, slots=slots, dt_bias=dt_bias, dt_min=dt_min,
+                                  dt_max=dt_max, out=out, state_out=state_out, path=path, workspace=workspace)
+    code = _DT.get(io)
+    if code is None:
         raise ValueError(f"x dtype {io} not supported (float32 or bfloat16)")
-    batch, L, H, P = x.shape
-    if not isinstance(B, torch.Tensor) or B.dim() != 4:
-        raise ValueError("B must be (batch, L, G, N)")
-    G, N = B.shape[2:]
-    _rows(dt, "dt", io, dev, (batch, L, H))
-    _rows(B, "B", io, dev, (batch, L, G, N))
-    _rows(C, "C", io, dev, (batch, L, G, N))
-    for t, name, dims in ((x, "x", 2), (dt, "dt", 1), (B, "B", 2), (C, "C", 2)):
-        _inner(t, name, dims)
+    batch, L, H, P = xshape
+    G, N = B.shape[2:] if isinstance(B, torch.Tensor) and B.dim() == 4 else (0, 0)
+    bc, vec, row = (batch, L, G, N), (H,), (batch,)
+    xs, ds = _rows(x, "x", io, dev, xshape, 2), _rows(dt, "dt", io, dev, (batch, L, H), 1)
+    bs, cs = _rows(B, "B", io, dev, bc, 2), _rows(C, "C", io, dev, bc, 2)
     if A is None:
         raise ValueError("A is required")
-    pa, pd, pb = (_vector(t, n, torch.float32, dev, H) for t, n in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")))
-    plen, pslot = (_vector(t, n, torch.int32, dev, batch) for t, n in ((seqlens, "seqlens"), (slots, "slots")))
-    rows = batch
-    if slots is not None:
-        if state_out is None:
-            state_out = init
-        if state_out is None:
+    pa, pd, pb = _whole(A, "A", _F32, dev, vec), _whole(D, "D", _F32, dev, vec), _whole(dt_bias, "dt_bias", _F32, dev, vec)
+    plen, pslot = _whole(seqlens, "seqlens", _I32, dev, row), _whole(slots, "slots", _I32, dev, row)
+    page = (H, P, N)
+    if state_out is None:
+        if slots is None:
+            state_out = x.new_empty((batch, *page), dtype=_F32)
+        elif init is None:
             raise ValueError("slots need a pool: init, state_out or both")
-        rows = state_out.shape[0]
-    elif state_out is None:
-        state_out = torch.empty(batch, H, P, N, dtype=torch.float32, device=dev)
-    _pool(state_out, "state_out", dev, rows, H, P, N)
-    if init is not None and init is not state_out:
-        _pool(init, "init", dev, rows, H, P, N)
-        _apart(init, state_out, "init", "state_out")
+        else:
+            state_out = init
+    rows = _states(state_out, "state_out", dev, slots, batch, page)
+    pinit = 0
+    if init is not None:
+        pinit = _whole(init, "init", _F32, dev, (rows, *page))
+        if init is not state_out:
+            _apart(init, state_out, "init", "state_out")
     if out is None:
-        out = torch.empty((batch, L, H, P), dtype=io, device=dev)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(xshape)
+        pout = out.data_ptr()
     else:
-        _need(out, "out", io, dev, 4)
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
-    xs, ds, bs, cs = x.stride(), dt.stride(), B.stride(), C.stride()
-    with _On(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        ws = _scratch(dev, stream, workspace)
-        nbytes = lib.ssd_workspace_bytes(SSD_OP_CAUSAL_FWD, batch, L, H, P, N, G, 0, _DT[io])
-        with ws.lock:
-            buf = ws.get(nbytes)
-            rc = lib.ssd_causal_fwd(x.data_ptr(), dt.data_ptr(), pa, B.data_ptr(), C.data_ptr(), pd, pb, dt_min, dt_max,
-                                    plen, pslot, init.data_ptr() if init is not None else 0, state_out.data_ptr(),
-                                    out.data_ptr(), xs[0], xs[1], ds[0], ds[1], bs[0], bs[1], cs[0], cs[1], rows,
-                                    batch, L, H, P, N, G, _DT[io], path, buf.data_ptr(), buf.numel(), stream)
+        pout = _whole(out, "out", io, dev, xshape)
+    stream = _raw_stream(dev.index)
+    ws = _scratch(dev, stream, workspace)
+    nbytes = _bytes(dev.index, SSD_OP_CAUSAL_FWD, batch, L, H, P, N, G, code)
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_causal_fwd(x.data_ptr(), dt.data_ptr(), pa, B.data_ptr(), C.data_ptr(), pd, pb, dt_min, dt_max, plen,
+                                pslot, pinit, state_out.data_ptr(), pout, xs[0], xs[1], ds[0], ds[1], bs[0], bs[1],
+                                cs[0], cs[1], rows, batch, L, H, P, N, G, code, path, buf.data_ptr(), buf.numel(), stream)
     _check(rc, "ssd_causal_fwd")
     return out, state_out
 
@@ -155,92 +175,82 @@ def ssd_causal_step(x, dt, A, B, C, D, states, slots=None, *, dt_bias=None, dt_m
     P), dt (batch, H), B, C (batch, G, N), D (H) or None. The states, (batch, H,
     P, N) or with slots (batch) int32 a pool of pages, advance in place unless
     state_out is given. Returns out like x."""
-    _need_cuda(x, "x", 3)
-    dev, io = x.device, x.dtype
-    if io not in _DT:
+    dev, io, xshape = _lead(x, "x", 3)
+    if dev.index != _device():
+        with torch.cuda.device(dev):
+            return ssd_causal_step(x, dt, A, B, C, D, states, slots, dt_bias=dt_bias, dt_min=dt_min, dt_max=dt_max,
+                                   out=out, state_out=state_out, workspace=workspace)
+    code = _DT.get(io)
+    if code is None:
         raise ValueError(f"x dtype {io} not supported (float32 or bfloat16)")
-    batch, H, P = x.shape
-    if not isinstance(B, torch.Tensor) or B.dim() != 3:
-        raise ValueError("B must be (batch, G, N)")
-    G, N = B.shape[1:]
-    _rows(dt, "dt", io, dev, (batch, H))
-    _rows(B, "B", io, dev, (batch, G, N))
-    _rows(C, "C", io, dev, (batch, G, N))
-    for t, name, dims in ((x, "x", 2), (dt, "dt", 1), (B, "B", 2), (C, "C", 2)):
-        _inner(t, name, dims)
+    batch, H, P = xshape
+    G, N = B.shape[1:] if isinstance(B, torch.Tensor) and B.dim() == 3 else (0, 0)
+    bc, vec = (batch, G, N), (H,)
+    xs, ds = _rows(x, "x", io, dev, xshape, 2), _rows(dt, "dt", io, dev, (batch, H), 1)
+    bs, cs = _rows(B, "B", io, dev, bc, 2), _rows(C, "C", io, dev, bc, 2)
     if A is None:
         raise ValueError("A is required")
-    pa, pd, pb = (_vector(t, n, torch.float32, dev, H) for t, n in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")))
-    pslot = _vector(slots, "slots", torch.int32, dev, batch)
-    _pool(states, "states", dev, batch if slots is None else None, H, P, N)
+    pa, pd, pb = _whole(A, "A", _F32, dev, vec), _whole(D, "D", _F32, dev, vec), _whole(dt_bias, "dt_bias", _F32, dev, vec)
+    page = (H, P, N)
+    rows = _states(states, "states", dev, slots, batch, page)
     if state_out is None:
         state_out = states
     elif state_out is not states:
-        _pool(state_out, "state_out", dev, states.shape[0], H, P, N)
+        _whole(state_out, "state_out", _F32, dev, (rows, *page))
         _apart(states, state_out, "states", "state_out")
     if out is None:
-        out = torch.empty((batch, H, P), dtype=io, device=dev)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(xshape)
+        pout = out.data_ptr()
     else:
-        _need(out, "out", io, dev, 3)
-        if out.shape != x.shape:
-            raise ValueError("out must have x's shape")
-    with _On(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        pws = nws = 0
-        if slots is not None:
-            ws = _scratch(dev, stream, workspace)
-            nbytes = 256 if batch <= 2048 else lib.ssd_workspace_bytes(SSD_OP_CAUSAL_STEP, batch, 1, H, P, N, G, 0, _DT[io])
-            ws.lock.acquire()
+        pout = _whole(out, "out", io, dev, xshape)
+    stream = _raw_stream(dev.index)
+    if slots is None:
+        rc = lib.ssd_causal_step(x.data_ptr(), dt.data_ptr(), pa, B.data_ptr(), C.data_ptr(), pd, pb, dt_min, dt_max, 0,
+                                 states.data_ptr(), state_out.data_ptr(), pout, xs[0], ds[0], bs[0], cs[0], rows, batch,
+                                 H, P, N, G, code, 0, 0, stream)
+    else:
+        pslot = _whole(slots, "slots", _I32, dev, (batch,))
+        ws = _scratch(dev, stream, workspace)
+        nbytes = _bytes(dev.index, SSD_OP_CAUSAL_STEP, batch, 1, H, P, N, G, code)
+        with ws.lock:
             buf = ws.get(nbytes)
-            pws, nws = buf.data_ptr(), buf.numel()
-        try:
             rc = lib.ssd_causal_step(x.data_ptr(), dt.data_ptr(), pa, B.data_ptr(), C.data_ptr(), pd, pb, dt_min, dt_max,
-                                     pslot, states.data_ptr(), state_out.data_ptr(), out.data_ptr(), x.stride(0),
-                                     dt.stride(0), B.stride(0), C.stride(0), states.shape[0], batch, H, P, N, G,
-                                     _DT[io], pws, nws, stream)
-        finally:
-            if slots is not None:
-                ws.lock.release()
+                                     pslot, states.data_ptr(), state_out.data_ptr(), pout, xs[0], ds[0], bs[0], cs[0], rows,
+                                     batch, H, P, N, G, code, buf.data_ptr(), buf.numel(), stream)
     _check(rc, "ssd_causal_step")
     return out
 
 
-def _need_cuda(t, name, ndim):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims (got {tuple(t.shape)})")
-
-
 def _pages(pool):
-    _need(pool, "pool")
-    if pool.dim() < 3:
-        raise ValueError(f"pool must be (layers, slots, page...) (got {tuple(pool.shape)})")
-    layers, nslots = pool.shape[:2]
-    page = pool.element_size()
-    for n in pool.shape[2:]:
-        page *= n
-    return layers, nslots, page
+    """Device, layers, slots and bytes of a page of a pool (layers, slots, page...)."""
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("pool must be a torch.Tensor")
+    dev, shape = pool.device, pool.shape
+    if dev.type != "cuda":
+        raise ValueError(f"pool must be a CUDA tensor (got {dev})")
+    if len(shape) < 3 or not pool.is_contiguous():
+        raise ValueError(f"pool must be (layers, slots, page...), contiguous (got {tuple(shape)}, strides {pool.stride()})")
+    layers, nslots = shape[0], shape[1]
+    return dev, layers, nslots, pool.element_size() * shape[2:].numel()
 
 
 def ssd_cache_copy(pool, src, dst, *, workspace: Workspace | None = None):
     """Pages of a pool (layers, slots, ...) of any dtype, in place and in every
     layer: page dst[i] <- page src[i], or zero where src[i] is -1, in the order
     of i (include/ssd_bidir.h: ssd_cache_copy). src, dst (n) int32. Returns pool."""
-    layers, nslots, page = _pages(pool)
-    dev = pool.device
-    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
+    dev, layers, nslots, page = _pages(pool)
+    if dev.index != _device():
+        with torch.cuda.device(dev):
+            return ssd_cache_copy(pool, src, dst, workspace=workspace)
     if src is None or dst is None:
         raise ValueError("src and dst are required")
-    ps, pd = _vector(src, "src", torch.int32, dev, n), _vector(dst, "dst", torch.int32, dev, n)
-    with _On(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        ws = _scratch(dev, stream, workspace)
-        with ws.lock:
-            buf = ws.get(256)
-            rc = lib.ssd_cache_copy(pool.data_ptr(), page, layers, nslots, ps, pd, n, buf.data_ptr(), buf.numel(), stream)
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
+    ps, pd = _whole(src, "src", _I32, dev, (n,)), _whole(dst, "dst", _I32, dev, (n,))
+    stream = _raw_stream(dev.index)
+    ws = _scratch(dev, stream, workspace)
+    with ws.lock:
+        buf = ws.get(256)
+        rc = lib.ssd_cache_copy(pool.data_ptr(), page, layers, nslots, ps, pd, n, buf.data_ptr(), buf.numel(), stream)
     _check(rc, "ssd_cache_copy")
     return pool
 
@@ -250,17 +260,22 @@ def ssd_cache_compact(pool, table, *, workspace: Workspace | None = None):
     pool (layers, slots, ...), in place, with the fewest moves (include/
     ssd_bidir.h: ssd_cache_compact). Returns (the table that goes with the moved
     pages, the number of live pages as an int32 tensor of one)."""
-    layers, nslots, page = _pages(pool)
-    dev = pool.device
-    _need(table, "table", torch.int32, dev, 1)
-    new = torch.empty_like(table)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    with _On(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        ws = _scratch(dev, stream, workspace)
-        with ws.lock:
-            buf = ws.get(256)
-            rc = lib.ssd_cache_compact(pool.data_ptr(), page, layers, nslots, table.data_ptr(), table.shape[0],
-                                       new.data_ptr(), live.data_ptr(), buf.data_ptr(), buf.numel(), stream)
+    dev, layers, nslots, page = _pages(pool)
+    if dev.index != _device():
+        with torch.cuda.device(dev):
+            return ssd_cache_compact(pool, table, workspace=workspace)
+    if table is None:
+        raise ValueError("table is required")
+    rows = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() == 1 else 0
+    ptable = _whole(table, "table", _I32, dev, (rows,))
+    # the new table and the count, which share an allocation
+    both = table.new_empty((rows + 1,))
+    pnew = both.data_ptr()
+    stream = _raw_stream(dev.index)
+    ws = _scratch(dev, stream, workspace)
+    with ws.lock:
+        buf = ws.get(256)
+        rc = lib.ssd_cache_compact(pool.data_ptr(), page, layers, nslots, ptable, rows, pnew, pnew + 4 * rows,
+                                   buf.data_ptr(), buf.numel(), stream)
     _check(rc, "ssd_cache_compact")
-    return new, live
+    return both[:rows], both[rows:]

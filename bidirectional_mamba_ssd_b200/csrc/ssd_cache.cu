@@ -3,14 +3,21 @@
 // fewest moves. Both only move bytes (two pages' worth a pair, one where a page
 // is cleared), so the floor is the copy bandwidth.
 //
-// Work items are (layer, kChunk bytes of the page, kGroup pairs). A thread owns
-// the same 16 bytes of the page in every pair of a group and holds the group's
-// loads in flight together. Pairs that stand apart (no page written twice, none
-// both read and written) spread over the groups; otherwise one thread applies
-// the whole list to its 16 bytes in order, which is the order's meaning and
-// needs no synchronisation.
+// Pairs that stand apart (no page written twice, none both read and written) are
+// moved in any order, by the bulk copy engine: one thread per SM keeps kAhead loads
+// of up to 16 KB on their way into shared memory and about as many stores on their
+// way out, with no data in registers. A page that is forked is loaded once for all
+// pairs in a row that name it; a page that is cleared is stored from a buffer of
+// zeros. Otherwise (and for pages that are not whole 16-byte pieces) threads own the
+// same element of the page in every pair; where pairs do not stand apart one
+// thread applies the whole list to its element in order, which is the order's
+// meaning and needs no synchronisation.
+// Measured on 16 pages to two others each and 8 cleared, 24 layers of 786 KB (1.06
+// GB): see the table of the kernel's figures; a copy through registers (8 loads of
+// 16 bytes a thread in flight) took 238 us.
 #include <stdint.h>
 
+#include "sm100.cuh"
 #include "ssd_causal.h"
 #include "ssd_kernels.h"
 
@@ -58,10 +65,117 @@ __device__ __forceinline__ void read_pair(const CacheArgs &a, int i, int &s, int
     if (bad || s == d) d = -1;
 }
 
+// ------------------------------------------------------------------ bulk copies
+constexpr int kPiece = 16384;     // bytes of a page moved at a time
+constexpr int kStages = 8;        // pieces in shared memory (the maps of the largest pool fit beside them)
+constexpr int kAhead = 4;         // loads on their way; the other stages are for stores
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+struct BulkSmem {
+    alignas(128) uint8_t piece[kStages][kPiece];
+    alignas(128) uint8_t zero[kPiece];
+    uint64_t bars[kStages];
+    struct Move {
+        int pair, bytes;           // pair < 0: nothing
+        long long at;              // byte offset of the piece in a page of the layer
+        char *layer;
+    } moves[kStages];
+};
+
+// One thread moves the CTA's share of (pair, layer, piece), pieces fastest.
+// pairs(i, s, next): the source of the i-th pair (-1: cleared; < -1: leave the pair
+// out) and one past the last of the pairs in a row that share it; dest(i): its page.
+template <typename Source, typename Dest>
+__device__ void bulk_move(BulkSmem &sm, const CacheArgs &a, int n, int abort_where, Source source, Dest dest) {
+    using namespace sm100;
+    const long long pieces = (a.page_bytes + kPiece - 1) / kPiece, per = pieces * a.layers;
+    const long long items = per * n;
+    auto bar = [&](int s) { return smem_u32(&sm.bars[s]); };
+    long long it = blockIdx.x;
+    int pair = -1, src = -2;
+    uint32_t k = 0;
+    bool more = true;
+    for (uint32_t done = 0; more || done < k;) {
+        // the next piece with something to move
+        if (more) {
+            more = false;
+            for (; it < items; it += gridDim.x) {
+                const int i = (int)(it / per);
+                if (i != pair) {
+                    pair = i;
+                    src = source(i);
+                }
+                if (src >= -1) {
+                    const int s = (int)(k % kStages);
+                    const long long piece = it % per;
+                    BulkSmem::Move &m = sm.moves[s];
+                    m.pair = i;
+                    m.at = piece % pieces * kPiece;
+                    m.layer = static_cast<char *>(a.pool) + piece / pieces * a.nslots * a.page_bytes;
+                    const long long left = a.page_bytes - m.at;
+                    m.bytes = (int)(left < kPiece ? left : kPiece);
+                    // the stores of the piece kStages ago have read its stage: of those made
+                    // since, kStages - kAhead - 1 may still be on their way
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStages - kAhead - 1) : "memory");
+                    if (src >= 0) {
+                        mbar_arrive_expect_tx(bar(s), m.bytes);
+                        bulk_load(smem_u32(sm.piece[s]), m.layer + src * a.page_bytes + m.at, m.bytes, bar(s));
+                    } else {
+                        mbar_arrive(bar(s));
+                    }
+                    ++k;
+                    it += gridDim.x;
+                    more = true;
+                    break;
+                }
+            }
+        }
+        // the oldest piece on its way, once there are enough behind it
+        if (done < k && (!more || k - done > kAhead)) {
+            const int s = (int)(done % kStages);
+            const BulkSmem::Move m = sm.moves[s];
+            WaitClock clock;
+            bool here = mbar_try_wait(bar(s), (done / kStages) & 1);
+            while (!here && !clock.expired(1000000000ull)) here = mbar_try_wait(bar(s), (done / kStages) & 1);
+            if (!here) {
+                more = false;
+                report_timeout(a.status, abort_where);
+                for (; done < k; ++done) mbar_drain(bar((int)(done % kStages)), (done / kStages) & 1);
+                break;
+            }
+            dest(m.pair, [&](int d, bool cleared) {
+                bulk_store(m.layer + d * a.page_bytes + m.at, smem_u32(cleared ? sm.zero : sm.piece[s]), m.bytes);
+            });
+            tma_store_commit();
+            ++done;
+        }
+    }
+    tma_store_wait_all();
+}
+
+__device__ __forceinline__ void bulk_init(BulkSmem &sm) {
+    using namespace sm100;
+    for (int i = threadIdx.x; i < kPiece / 16; i += kThreads) reinterpret_cast<uint4 *>(sm.zero)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < kStages) mbar_init(smem_u32(&sm.bars[threadIdx.x]), 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    __syncthreads();
+}
+
 template <typename V>
 __global__ void __launch_bounds__(kThreads)
 cache_copy_kernel(const CacheArgs a) {
-    extern __shared__ uint32_t map[];      // written pages, one bit each
+    extern __shared__ __align__(128) uint8_t shared[];
+    // written pages, one bit each; where bulk copies may run their stages come first
+    uint32_t *map = reinterpret_cast<uint32_t *>(shared + (sizeof(V) == 16 ? sizeof(BulkSmem) : 0));
     __shared__ int ps[kGroup], pd[kGroup];
     const int tid = threadIdx.x;
     const long long elems = a.page_bytes / (long long)sizeof(V);
@@ -85,6 +199,36 @@ cache_copy_kernel(const CacheArgs a) {
         if (d >= 0 && s >= 0) clash |= (map[s >> 5] >> (s & 31)) & 1u;
     }
     clash = __syncthreads_or(clash);
+    if constexpr (sizeof(V) == 16) {
+        if (!clash) {
+            BulkSmem &sm = *reinterpret_cast<BulkSmem *>(shared);
+            bulk_init(sm);
+            if (tid == 0) {
+                auto valid = [&](int i, int &s, int &d) {
+                    bool bad;
+                    read_pair(a, i, s, d, bad);
+                    return !bad;
+                };
+                bulk_move(
+                    sm, a, a.n, 950,
+                    [&](int i) {
+                        int s, d, s0, d0;
+                        if (!valid(i, s, d)) return -2;
+                        if (s < 0) return d < 0 ? -2 : -1;
+                        // the first of the pairs in a row with this source loads for all
+                        return i > 0 && valid(i - 1, s0, d0) && s0 == s ? -2 : s;
+                    },
+                    [&](int i, auto store) {
+                        int s, d, s0, d0;
+                        valid(i, s, d);
+                        if (s < 0) return store(d, true);
+                        for (int q = i; q < a.n && valid(q, s0, d0) && s0 == s; ++q)
+                            if (d0 >= 0) store(d0, false);
+                    });
+            }
+            return;
+        }
+    }
     const int groups = clash ? 1 : (a.n + kGroup - 1) / kGroup;
     const long long items = (long long)a.layers * chunks * groups;
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -130,7 +274,8 @@ __device__ __forceinline__ int select_bit(const uint32_t *map, const int *before
 template <typename V>
 __global__ void __launch_bounds__(kThreads)
 cache_compact_kernel(const CacheArgs a) {
-    extern __shared__ uint32_t map[];
+    extern __shared__ __align__(128) uint8_t shared[];
+    uint32_t *map = reinterpret_cast<uint32_t *>(shared + (sizeof(V) == 16 ? sizeof(BulkSmem) : 0));
     __shared__ int ps[kGroup], pd[kGroup], part[kThreads], sum_live, sum_moves;
     const int tid = threadIdx.x;
     const int words = (a.nslots + 31) / 32;
@@ -188,6 +333,15 @@ cache_compact_kernel(const CacheArgs a) {
             a.table_out[i] = in && s >= live ? target(rank(s) - stay) : in ? s : -1;
         }
     }
+    if constexpr (sizeof(V) == 16) {
+        BulkSmem &sm = *reinterpret_cast<BulkSmem *>(shared);
+        bulk_init(sm);
+        if (tid == 0)
+            bulk_move(
+                sm, a, moves, 951, [&](int i) { return select_bit<true>(map, before, words, stay + i); },
+                [&](int i, auto store) { store(target(i), false); });
+        return;
+    }
     const long long elems = a.page_bytes / (long long)sizeof(V);
     const long long chunks = (elems + kThreads - 1) / kThreads;
     const int groups = (moves + kGroup - 1) / kGroup;
@@ -207,34 +361,31 @@ cache_compact_kernel(const CacheArgs a) {
     }
 }
 
-template <typename V>
-cudaError_t copy_v(const CacheArgs &a, cudaStream_t stream) {
-    const size_t smem = (size_t)((a.nslots + 31) / 32) * 4;
-    cudaError_t e;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(cache_copy_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return e;
-    const long long chunks = (a.page_bytes / (long long)sizeof(V) + kThreads - 1) / kThreads;
-    const long long items = chunks * a.layers * ((a.n + kGroup - 1) / kGroup);
-    const long long most = 8LL * device_sms();
-    cache_copy_kernel<V><<<(unsigned)(items < most ? items : most), kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
-}
-
-template <typename V>
-cudaError_t compact_v(const CacheArgs &a, cudaStream_t stream) {
-    const size_t smem = (size_t)((a.nslots + 31) / 32) * 8;
+// Shared memory and grid: with bulk copies one CTA per SM, else eight.
+template <typename V, typename K>
+cudaError_t launch(K kernel, const CacheArgs &a, long long pairs, size_t maps, cudaStream_t stream) {
+    constexpr bool kBulk = sizeof(V) == 16;
+    const size_t smem = maps + (kBulk ? sizeof(BulkSmem) : 0);
     cudaError_t e;
     if (smem > 40 * 1024 &&
-        (e = cudaFuncSetAttribute(cache_compact_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
         return e;
-    const long long chunks = (a.page_bytes / (long long)sizeof(V) + kThreads - 1) / kThreads;
+    static_assert(!kBulk || sizeof(BulkSmem) + kCacheMaxSlots / 32 * 8 <= 232448 - 2048, "stages and maps in shared memory");
+    const long long per = kBulk ? (a.page_bytes + kPiece - 1) / kPiece * pairs
+                                : (a.page_bytes / (long long)sizeof(V) + kThreads - 1) / kThreads * ((pairs + kGroup - 1) / kGroup);
+    const long long items = per * a.layers, most = (kBulk ? 1LL : 8LL) * device_sms();
+    kernel<<<(unsigned)(items < 1 ? 1 : items < most ? items : most), kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+template <typename V>
+cudaError_t copy_v(const CacheArgs &a, cudaStream_t stream) {
+    return launch<V>(cache_copy_kernel<V>, a, a.n, (size_t)((a.nslots + 31) / 32) * 4, stream);
+}
+template <typename V>
+cudaError_t compact_v(const CacheArgs &a, cudaStream_t stream) {
     // no more moves than half the pages or than rows of the table
     const long long moves = a.rows < a.nslots / 2 ? a.rows : a.nslots / 2;
-    const long long items = chunks * a.layers * ((moves + kGroup - 1) / kGroup);
-    const long long most = 8LL * device_sms();
-    cache_compact_kernel<V><<<(unsigned)(items < 1 ? 1 : items < most ? items : most), kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch<V>(cache_compact_kernel<V>, a, moves, (size_t)((a.nslots + 31) / 32) * 8, stream);
 }
 
 int width(const CacheArgs &a) {
@@ -244,7 +395,7 @@ int width(const CacheArgs &a) {
 
 }  // namespace
 
-// 16 bytes a thread where the pages allow it, else 4 or 1 (pages of odd sizes)
+// Bulk copies where the pages are whole 16-byte pieces, else 4 or 1 bytes a thread.
 cudaError_t launch_cache_copy(const CacheArgs &a, cudaStream_t stream) {
     if (device_sms() < 1) return cudaErrorNotSupported;
     const int w = width(a);

@@ -95,7 +95,7 @@ struct CacheArgs {
     int *table_out, *live_out;
     DeviceStatus *status;
 };
-constexpr int kCacheMaxSlots = 1 << 19;   // two 64 KB maps in shared memory
+constexpr int kCacheMaxSlots = 1 << 18;   // two 32 KB maps in shared memory
 cudaError_t launch_cache_copy(const CacheArgs &a, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CacheArgs &a, cudaStream_t stream);
 

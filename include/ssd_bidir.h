@@ -460,7 +460,7 @@ int ssd_causal_step(const void *x, const void *dt, const float *A, const void *B
  * where src[i] is -1 (a freed page). One source with several destinations
  * forks it; the order also defines chains and repeated destinations. dst[i] =
  * -1 leaves the pair out; so does an index outside [-1, nslots), reported as
- * SSD_ERR_INDEX. src, dst (n) int32 in device memory. nslots <= 524288.
+ * SSD_ERR_INDEX. src, dst (n) int32 in device memory. nslots <= 262144.
  * Workspace: the 256-byte status header. */
 int ssd_cache_copy(void *pool, long long page_bytes, int layers, int nslots, const int *src, const int *dst, int n,
                    void *workspace, size_t ws_bytes, void *stream);

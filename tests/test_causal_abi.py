@@ -75,13 +75,13 @@ def test_step_and_cache_entry_points_reject_bad_arguments(lib):
         return lib.ssd_cache_copy(v(pool), page, layers, nslots, v(src), v(dst), n, v(ws), wsb, None)
 
     assert copy(page=-1) == -1 and copy(n=-1) == -1 and copy(nslots=-1) == -1 and copy(layers=-1) == -1
-    assert copy(nslots=(1 << 19) + 1) == -2 and copy(ws=0) == -4 and copy(wsb=8) == -4
+    assert copy(nslots=(1 << 18) + 1) == -2 and copy(ws=0) == -4 and copy(wsb=8) == -4
     assert copy(pool=0) == -1 and copy(src=0) == -1 and copy(dst=FAKE + 2) == -1
     assert copy(n=0, src=0, dst=0, pool=0) == 0 and copy(page=0, pool=0) == 0
 
     def compact(pool=FAKE, page=64, layers=2, nslots=4, table=FAKE, rows=3, out=FAKE + 64, live=FAKE, ws=FAKE, wsb=256):
         return lib.ssd_cache_compact(v(pool), page, layers, nslots, v(table), rows, v(out), v(live), v(ws), wsb, None)
 
-    assert compact(rows=-1) == -1 and compact(nslots=(1 << 19) + 1) == -2 and compact(ws=0) == -4
+    assert compact(rows=-1) == -1 and compact(nslots=(1 << 18) + 1) == -2 and compact(ws=0) == -4
     assert compact(pool=0) == -1 and compact(table=0) == -1 and compact(out=0) == -1 and compact(live=0) == -1
     assert compact(out=FAKE) == -1 and compact(out=FAKE + 8) == -1       # the tables overlap
