@@ -4,9 +4,9 @@
 // is cleared), so the floor is the copy bandwidth.
 //
 // Pairs that stand apart (no page written twice, none both read and written) are
-// moved in any order, by the bulk copy engine: one thread per SM keeps kAhead loads
-// of up to 16 KB on their way into shared memory and about as many stores on their
-// way out, with no data in registers. A page that is forked is loaded once for all
+// moved in any order, by the bulk copy engine: kMovers threads of a CTA (one per SM)
+// each keep kAhead loads of up to 16 KB on their way into shared memory and about as
+// many stores on their way out, with no data in registers. A page that is forked is loaded once for all
 // pairs in a row that name it; a page that is cleared is stored from a buffer of
 // zeros. Otherwise (and for pages that are not whole 16-byte pieces) threads own the
 // same element of the page in every pair; where pairs do not stand apart one
@@ -67,8 +67,10 @@ __device__ __forceinline__ void read_pair(const CacheArgs &a, int i, int &s, int
 
 // ------------------------------------------------------------------ bulk copies
 constexpr int kPiece = 16384;     // bytes of a page moved at a time
-constexpr int kStages = 8;        // pieces in shared memory (the maps of the largest pool fit beside them)
-constexpr int kAhead = 4;         // loads on their way; the other stages are for stores
+constexpr int kMovers = 2;        // threads of a CTA that move pieces, each its own
+constexpr int kStages = 4;        // pieces of a mover in shared memory (the maps of the largest pool fit beside them)
+constexpr int kAhead = 2;         // loads of a mover on their way; the other stages are for stores
+constexpr int kListed = 1024;     // pairs kept in shared memory; a longer list is read where it is
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -80,46 +82,53 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
 }
 
 struct BulkSmem {
-    alignas(128) uint8_t piece[kStages][kPiece];
+    alignas(128) uint8_t piece[kMovers][kStages][kPiece];
     alignas(128) uint8_t zero[kPiece];
-    uint64_t bars[kStages];
+    uint64_t bars[kMovers][kStages];
     struct Move {
-        int pair, bytes;           // pair < 0: nothing
+        int pair, dst, bytes;
         long long at;              // byte offset of the piece in a page of the layer
         char *layer;
-    } moves[kStages];
+    } moves[kMovers][kStages];
+    int2 list[kListed];
 };
 
-// One thread moves the CTA's share of (pair, layer, piece), pieces fastest.
-// pairs(i, s, next): the source of the i-th pair (-1: cleared; < -1: leave the pair
-// out) and one past the last of the pairs in a row that share it; dest(i): its page.
+// One thread (mover w of its CTA) moves its share of (pair, layer, piece), pieces
+// fastest. source(i, dst): the source of the i-th pair (-1: cleared; < -1: leave the
+// pair out) and its first destination; dest(i, dst, store): store(d, cleared) for
+// every page d that the piece goes to.
 template <typename Source, typename Dest>
-__device__ void bulk_move(BulkSmem &sm, const CacheArgs &a, int n, int abort_where, Source source, Dest dest) {
+__device__ void bulk_move(BulkSmem &sm, const CacheArgs &a, int w, int n, int abort_where, Source source, Dest dest) {
     using namespace sm100;
-    const long long pieces = (a.page_bytes + kPiece - 1) / kPiece, per = pieces * a.layers;
-    const long long items = per * n;
-    auto bar = [&](int s) { return smem_u32(&sm.bars[s]); };
-    long long it = blockIdx.x;
-    int pair = -1, src = -2;
+    // Where the mover is in (pair, layer, piece), and its stride: all movers, written in
+    // the same digits, so that a step is additions only (divisions of 64 bits a piece cost
+    // more than the piece).
+    const long long pieces = (a.page_bytes + kPiece - 1) / kPiece;
+    const long long all = (long long)gridDim.x * kMovers, me = (long long)w * gridDim.x + blockIdx.x;
+    const long long dpiece = all % pieces, dlayer = all / pieces % a.layers, dpair = all / pieces / a.layers;
+    long long piece = me % pieces, layer = me / pieces % a.layers, pair = me / pieces / a.layers;
+    const long long layer_bytes = (long long)a.nslots * a.page_bytes;
+    auto bar = [&](int s) { return smem_u32(&sm.bars[w][s]); };
+    int at = -1, src = -2, dst = -1;             // the pair that src belongs to
     uint32_t k = 0;
     bool more = true;
     for (uint32_t done = 0; more || done < k;) {
         // the next piece with something to move
         if (more) {
             more = false;
-            for (; it < items; it += gridDim.x) {
-                const int i = (int)(it / per);
-                if (i != pair) {
-                    pair = i;
-                    src = source(i);
+            while (pair < n && !more) {
+                const int i = (int)pair;
+                if (i != at) {
+                    at = i;
+                    src = source(i, dst);
                 }
                 if (src >= -1) {
                     const int s = (int)(k % kStages);
-                    const long long piece = it % per;
-                    BulkSmem::Move &m = sm.moves[s];
+                    BulkSmem::Move &m = sm.moves[w][s];
                     m.pair = i;
-                    m.at = piece % pieces * kPiece;
-                    m.layer = static_cast<char *>(a.pool) + piece / pieces * a.nslots * a.page_bytes;
+                    m.dst = dst;
+                    m.at = piece * kPiece;
+                    m.layer = static_cast<char *>(a.pool) + layer * layer_bytes;
                     const long long left = a.page_bytes - m.at;
                     m.bytes = (int)(left < kPiece ? left : kPiece);
                     // the stores of the piece kStages ago have read its stage: of those made
@@ -127,32 +136,43 @@ __device__ void bulk_move(BulkSmem &sm, const CacheArgs &a, int n, int abort_whe
                     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStages - kAhead - 1) : "memory");
                     if (src >= 0) {
                         mbar_arrive_expect_tx(bar(s), m.bytes);
-                        bulk_load(smem_u32(sm.piece[s]), m.layer + src * a.page_bytes + m.at, m.bytes, bar(s));
+                        bulk_load(smem_u32(sm.piece[w][s]), m.layer + src * a.page_bytes + m.at, m.bytes, bar(s));
                     } else {
                         mbar_arrive(bar(s));
                     }
                     ++k;
-                    it += gridDim.x;
                     more = true;
-                    break;
+                }
+                piece += dpiece;
+                layer += dlayer;
+                pair += dpair;
+                if (piece >= pieces) {
+                    piece -= pieces;
+                    ++layer;
+                }
+                if (layer >= a.layers) {
+                    layer -= a.layers;
+                    ++pair;
                 }
             }
         }
         // the oldest piece on its way, once there are enough behind it
         if (done < k && (!more || k - done > kAhead)) {
             const int s = (int)(done % kStages);
-            const BulkSmem::Move m = sm.moves[s];
-            WaitClock clock;
+            const BulkSmem::Move m = sm.moves[w][s];
             bool here = mbar_try_wait(bar(s), (done / kStages) & 1);
-            while (!here && !clock.expired(1000000000ull)) here = mbar_try_wait(bar(s), (done / kStages) & 1);
+            if (!here) {
+                WaitClock clock;
+                while (!here && !clock.expired(1000000000ull)) here = mbar_try_wait(bar(s), (done / kStages) & 1);
+            }
             if (!here) {
                 more = false;
                 report_timeout(a.status, abort_where);
                 for (; done < k; ++done) mbar_drain(bar((int)(done % kStages)), (done / kStages) & 1);
                 break;
             }
-            dest(m.pair, [&](int d, bool cleared) {
-                bulk_store(m.layer + d * a.page_bytes + m.at, smem_u32(cleared ? sm.zero : sm.piece[s]), m.bytes);
+            dest(m.pair, m.dst, [&](int d, bool cleared) {
+                bulk_store(m.layer + d * a.page_bytes + m.at, smem_u32(cleared ? sm.zero : sm.piece[w][s]), m.bytes);
             });
             tma_store_commit();
             ++done;
@@ -164,7 +184,7 @@ __device__ void bulk_move(BulkSmem &sm, const CacheArgs &a, int n, int abort_whe
 __device__ __forceinline__ void bulk_init(BulkSmem &sm) {
     using namespace sm100;
     for (int i = threadIdx.x; i < kPiece / 16; i += kThreads) reinterpret_cast<uint4 *>(sm.zero)[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x < kStages) mbar_init(smem_u32(&sm.bars[threadIdx.x]), 1);
+    if (threadIdx.x < kMovers * kStages) mbar_init(smem_u32(&sm.bars[0][0] + threadIdx.x), 1);
     fence_mbar_init();
     fence_proxy_async_smem();
     __syncthreads();
@@ -202,30 +222,35 @@ cache_copy_kernel(const CacheArgs a) {
     if constexpr (sizeof(V) == 16) {
         if (!clash) {
             BulkSmem &sm = *reinterpret_cast<BulkSmem *>(shared);
+            // (source, destination) of a pair; a source of -2 leaves it out
+            auto fetch = [&](int i) {
+                int s, d;
+                bool bad;
+                read_pair(a, i, s, d, bad);
+                return make_int2(bad ? -2 : s, d);
+            };
+            for (int i = tid; i < min(a.n, kListed); i += kThreads) sm.list[i] = fetch(i);
             bulk_init(sm);
-            if (tid == 0) {
-                auto valid = [&](int i, int &s, int &d) {
-                    bool bad;
-                    read_pair(a, i, s, d, bad);
-                    return !bad;
-                };
+            auto pair = [&](int i) { return i < kListed ? sm.list[i] : fetch(i); };
+            if (tid % 32 == 0 && tid < 32 * kMovers)
                 bulk_move(
-                    sm, a, a.n, 950,
-                    [&](int i) {
-                        int s, d, s0, d0;
-                        if (!valid(i, s, d)) return -2;
-                        if (s < 0) return d < 0 ? -2 : -1;
+                    sm, a, tid / 32, a.n, 950,
+                    [&](int i, int &dst) {
+                        const int2 p = pair(i);
+                        dst = p.y;
+                        if (p.x < 0) return p.y < 0 ? -2 : p.x;
                         // the first of the pairs in a row with this source loads for all
-                        return i > 0 && valid(i - 1, s0, d0) && s0 == s ? -2 : s;
+                        return i > 0 && pair(i - 1).x == p.x ? -2 : p.x;
                     },
-                    [&](int i, auto store) {
-                        int s, d, s0, d0;
-                        valid(i, s, d);
-                        if (s < 0) return store(d, true);
-                        for (int q = i; q < a.n && valid(q, s0, d0) && s0 == s; ++q)
-                            if (d0 >= 0) store(d0, false);
+                    [&](int i, int dst, auto store) {
+                        const int src = pair(i).x;
+                        if (src < 0) return store(dst, true);
+                        for (int q = i; q < a.n; ++q) {
+                            const int2 p = pair(q);
+                            if (p.x != src) break;
+                            if (p.y >= 0) store(p.y, false);
+                        }
                     });
-            }
             return;
         }
     }
@@ -336,10 +361,14 @@ cache_compact_kernel(const CacheArgs a) {
     if constexpr (sizeof(V) == 16) {
         BulkSmem &sm = *reinterpret_cast<BulkSmem *>(shared);
         bulk_init(sm);
-        if (tid == 0)
+        if (tid % 32 == 0 && tid < 32 * kMovers)
             bulk_move(
-                sm, a, moves, 951, [&](int i) { return select_bit<true>(map, before, words, stay + i); },
-                [&](int i, auto store) { store(target(i), false); });
+                sm, a, tid / 32, moves, 951,
+                [&](int i, int &dst) {
+                    dst = target(i);
+                    return select_bit<true>(map, before, words, stay + i);
+                },
+                [&](int, int dst, auto store) { store(dst, false); });
         return;
     }
     const long long elems = a.page_bytes / (long long)sizeof(V);
