@@ -242,12 +242,13 @@ struct Walk {
 template <int N, bool STATE>
 struct Layout {
     static constexpr int kX = 3;                           // x slots
+    static constexpr int kRing = STATE ? 3 : 4;            // B (and C) slots of 32 KB
     static constexpr uint32_t kBC = N * 256;               // bytes of a B or C tile
-    static constexpr uint32_t ring = 0;                    // 4 slots of 32 KB
-    static constexpr uint32_t x0 = 4 * 2 * kSlab;
+    static constexpr uint32_t ring = 0;
+    static constexpr uint32_t x0 = kRing * 2 * kSlab;
     static constexpr uint32_t h = x0 + kX * kSlab;         // bf16 (N, 64) state
-    static constexpr uint32_t xw = h + (STATE ? 0 : kSlab);   // the three terms of half a tile of diag(w) X
-    static constexpr uint32_t small = xw + 3 * kHalf;
+    static constexpr uint32_t xw = h + (STATE ? 0 : kSlab);   // the three terms of half a tile of diag(w) X; STATE: of both
+    static constexpr uint32_t small = xw + (STATE ? 2 : 1) * 3 * kHalf;
 };
 
 enum {
@@ -258,9 +259,9 @@ enum {
     B_G_FREE = 22,       // 2: output groups -> MMA: the tile's TMEM buffers are read
     B_VEC_READY = 24,    // kVec: warp 2 -> C and the output groups
     B_VEC_FREE = 28,     // kVec: C and the output groups -> warp 2
-    B_XW_READY = 32,     // C -> MMA, twice a tile
-    B_S_READY,           // MMA -> C, twice a tile
-    B_H_READY,           // C -> MMA
+    B_XW_READY = 32,     // 2: C -> MMA: a half of diag(w) X of the tile
+    B_S_READY = 34,      // 2: MMA -> C: S of that half (and all before it)
+    B_H_READY = 36,      // C -> MMA
     B_DONE,
     B_COUNT
 };
@@ -417,11 +418,13 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     const uint32_t nsteps = __shfl_sync(0xffffffffu, (uint32_t)sm.nsteps, 0);
     auto tG = [&](uint32_t n) { return tmem + 128 * (n & 1); };
     auto tY = [&](uint32_t n) { return tmem + 256 + 64 * (n & 1); };
-    const uint32_t tS = tmem + 384;
+    // with no G and Y there is room for two S: the one is read while the other fills
+    auto tS = [&](uint32_t n) { return STATE ? tmem + 128 * (n & 1) : tmem + 384; };
+    auto xwbuf = [&](uint32_t hf) { return S::xw + (STATE ? hf * 3 * kHalf : 0); };
     // ring slots and their use counts
     auto slot_c = [](uint32_t n) { return (2 * n) & 3; };
-    auto slot_b = [](uint32_t n) { return STATE ? n & 3 : (2 * n + 1) & 3; };
-    auto use_bc = [](uint32_t n) { return STATE ? n >> 2 : n >> 1; };
+    auto slot_b = [](uint32_t n) { return STATE ? n % (uint32_t)S::kRing : (2 * n + 1) & 3; };
+    auto use_bc = [](uint32_t n) { return STATE ? n / (uint32_t)S::kRing : n >> 1; };
     auto slot_x = [](uint32_t n) { return n % (uint32_t)kX; };
     auto use_x = [](uint32_t n) { return n / (uint32_t)kX; };
     auto ring = [&](uint32_t s) { return base + S::ring + s * 2 * kSlab; };
@@ -455,7 +458,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     tma_load_4d(ring(s) + sl * kSlab, &tm_b, bar(B_RING_FULL + s), 64 * sl, grp, t0, w.b);
             }
             // every load issued has landed before the CTA may exit: the last use of each slot
-            constexpr uint32_t kDeep = STATE ? 4 : 2;
+            constexpr uint32_t kDeep = STATE ? S::kRing : 2;
             for (uint32_t q = n > kDeep ? n - kDeep : 0; q < n; ++q) {
                 if (!STATE) mbar_drain(bar(B_RING_FULL + slot_c(q)), use_bc(q) & 1);
                 mbar_drain(bar(B_RING_FULL + slot_b(q)), use_bc(q) & 1);
@@ -472,7 +475,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // descriptors of the fixed buffers and of ring and x slot 0: another slot,
             // and a K step, only add to the start address (in 16-byte units)
             const uint64_t mn = sdesc_sw128(base, kSlab, 1024), kmaj = sdesc_sw128(base, 0, 1024);
-            const uint64_t d_xw = sdesc_sw128(base + S::xw, kHalf, 1024), d_h = mn + (S::h >> 4);
+            const uint64_t d_xw = sdesc_sw128(base, kHalf, 1024), d_h = mn + (S::h >> 4);
             auto step_mn = [](int q) { return (uint64_t)(q * 128); };                             // 16 rows of 128 bytes
             auto step_k = [](int q) { return (uint64_t)((q >> 2) * (kSlab >> 4) + (q & 3) * 2); };   // 32 bytes; the next slab
             uint32_t nG = 0, mS = 0, nY = 0;     // mS: halves of tiles
@@ -482,16 +485,16 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 bool moved = false;
                 // S(n), half by half: B^T times the three terms of diag(w) X
                 const uint32_t nS = mS >> 1, hf = mS & 1;
-                if (nS < nsteps && mbar_test(bar(B_XW_READY), hf) &&
+                if (nS < nsteps && mbar_test(bar(B_XW_READY + hf), nS & 1) &&
                     (hf || mbar_test(bar(B_RING_FULL + slot_b(nS)), use_bc(nS) & 1))) {
                     tc_fence_after();
                     const uint64_t dB = mn + ((S::ring + slot_b(nS) * 2 * kSlab + hf * kHalf) >> 4);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        mma_bf16_ss(tS, dB + step_mn(q), d_xw + step_mn(q), id_s2, q ? 1u : hf);
-                        mma_bf16_ss(tS + 64, dB + step_mn(q), d_xw + 2 * (kHalf >> 4) + step_mn(q), id_s1, 1u);
+                        mma_bf16_ss(tS(nS), dB + step_mn(q), d_xw + (xwbuf(hf) >> 4) + step_mn(q), id_s2, q ? 1u : hf);
+                        mma_bf16_ss(tS(nS) + 64, dB + step_mn(q), d_xw + ((xwbuf(hf) + 2 * kHalf) >> 4) + step_mn(q), id_s1, 1u);
                     }
-                    mma_commit(bar(B_S_READY));
+                    mma_commit(bar(B_S_READY + hf));
                     // B goes free with the second of its two readers, S and G
                     if (hf && (STATE || nG > nS)) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
                     ++mS;
@@ -668,7 +671,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             auto build = [&](int hf) {
                 const int r = hf * 64 + br;
                 uint8_t *xt = g + xslot(n) + r * 128;
-                uint8_t *dst = g + S::xw + br * 128;
+                uint8_t *dst = g + xwbuf(hf) + br * 128;
                 if (t0 + r < len) {
                     const float wt = I.w[r];
 #pragma unroll
@@ -694,18 +697,16 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 }
                 fence_proxy_async_smem();
                 sync_state();
-                if (cid == 0) mbar_arrive(bar(B_XW_READY));
+                if (cid == 0) mbar_arrive(bar(B_XW_READY + hf));
             };
-            // S of the tile before is complete (and has read its terms):
-            // H <- exp(a_T) H + S
-            if (n >= 1) {
-                mbar_wait_ool(bar(B_S_READY), 1, abort_flag, p.status, 924);
+            // H <- exp(a_T) H + S of the tile before
+            auto advance = [&]() {
                 tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t sv[2][8];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) tmem_ld8(tS + 64 * k + lane_off + q * 8, sv[k]);
+                    for (int k = 0; k < 2; ++k) tmem_ld8(tS(n - 1) + 64 * k + lane_off + q * 8, sv[k]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -713,8 +714,19 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                                             add2(pair_of(sv[0][2 * j], sv[0][2 * j + 1]), pair_of(sv[1][2 * j], sv[1][2 * j + 1])));
                 }
                 tc_fence_before();
-            }
+            };
+            // one buffer for diag(w) X and one S: a half waits for the half before, and S is
+            // read ahead of the first. Two of each: a half waits for its like of the tile before.
+            if (n >= 1) mbar_wait_ool(bar(B_S_READY + !STATE), (n - 1) & 1, abort_flag, p.status, 924);
+            if (!STATE && n >= 1) advance();
             if (tile) build(0);
+            if (STATE && n >= 1) {
+                mbar_wait_ool(bar(B_S_READY + 1), (n - 1) & 1, abort_flag, p.status, 928);
+                if (tile) build(1);
+                advance();
+            } else if (STATE && tile) {
+                build(1);
+            }
             if (n >= 1) {
                 if (pflags & kLast) {
                     // the state behind the unit or the part of it: the end state, or to the CTA
@@ -778,9 +790,9 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             pflags = flags;
             pb = I.b;
             phu = I.hu;
-            mbar_wait_ool(bar(B_S_READY), 0, abort_flag, p.status, 927);
-            build(1);
             if (!STATE) {
+                mbar_wait_ool(bar(B_S_READY), n & 1, abort_flag, p.status, 927);
+                build(1);
                 // C H of the tile before has read the buffer
                 if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
                 if (row < N && !(flags & kZeroStart)) {
