@@ -11,10 +11,11 @@
 //
 // The decay between two tokens is split at the tile's half decay a_r = a_T / 2:
 //   exp(a_t - a_s) = exp(a_t - a_r) * exp(a_r - a_s)
-// so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, and the row's
-// factor is applied to the fp32 output. Both stay within e^+-60 while the tile's
-// decay is at most 120; past that (a test on the tile) each entry takes its own
-// exponential.
+// so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, C H is taken of
+// exp(a_r) H, both add up in one accumulator, and the row's factor exp(a_t - a_r) is
+// applied to the fp32 sum. The factors stay within e^+-60 while the tile's decay is
+// at most 120; past that (a test on the tile) each entry of M takes its own
+// exponential and C H its own accumulator.
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
 // products whose result is rounded to bf16 (relative 2^-9 a term, random). The
@@ -36,13 +37,15 @@
 // rows n of it a thread, 32 columns each; warps 12..15 and 16..19 groups A and B:
 // mask and output of the even and the odd tiles, so that one tile's mask overlaps
 // the other's products and output; thread r owns tile row r.
-// TMEM (512 columns): two of {G 128: M packed over its first half once read, Yo over
-// its second}, two Y, S in two parts (the first term of diag(w) X and the other two:
-// an MMA with N = 128 reads B^T once for two terms). Shared memory: C and B two tiles
-// deep, x three, H once, the three terms of half a tile of diag(w) X.
+// TMEM (512 columns): two of {G 128: M packed over its first half once read, Y over
+// its second}, S 192 (the three terms of diag(w) X side by side: an MMA with N = 192
+// reads B^T once for all of them), Yo 64 for tiles past the one-factor mask. Shared
+// memory: C and B two tiles deep, x three, H once, the three terms of half a tile of
+// diag(w) X.
 // Every wait is bounded; one that expires sets the workspace's timeout flag and
 // the CTA runs to its end without storing.
 #include <cuda.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "sm100.cuh"
@@ -270,11 +273,13 @@ enum {
 // factors of M (the step sizes where each entry takes its own exponential), the
 // weights in the state.
 enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64 };
-struct TileInfo {
+struct alignas(16) TileInfo {
     float a[kTile], col[kTile], w[kTile];
     int b, h, hu, t0, len, flags;
-    float decay, D;      // exp(a_T); the head's skip factor
+    float decay, half, D;   // exp(a_T); the factor of H in C H: exp(a_r), or 1; the head's skip factor
 };
+
+static_assert(sizeof(TileInfo) % 16 == 0 && offsetof(TileInfo, col) % 16 == 0, "read 16 bytes at a time");
 
 struct Small {
     uint64_t bars[B_COUNT];
@@ -283,7 +288,7 @@ struct Small {
     int nsteps;
     int pad;
     Stage stages[3];
-    alignas(16) TileInfo info[kVec];
+    TileInfo info[kVec];
 };
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -417,9 +422,10 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     const uint32_t nsteps = __shfl_sync(0xffffffffu, (uint32_t)sm.nsteps, 0);
     auto tG = [&](uint32_t n) { return tmem + 128 * (n & 1); };
-    auto tY = [&](uint32_t n) { return tmem + 256 + 64 * (n & 1); };
+    auto tY = [&](uint32_t n) { return tG(n) + 64; };
+    const uint32_t tYo = tmem + 448;
     // with no G and Y there is room for two S: the one is read while the other fills
-    auto tS = [&](uint32_t n) { return STATE ? tmem + 128 * (n & 1) : tmem + 384; };
+    auto tS = [&](uint32_t n) { return STATE ? tmem + 192 * (n & 1) : tmem + 256; };
     auto xwbuf = [&](uint32_t hf) { return S::xw + (STATE ? hf * 3 * kHalf : 0); };
     // ring slots and their use counts
     auto slot_c = [](uint32_t n) { return (2 * n) & 3; };
@@ -468,8 +474,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (elect_one()) {
-            constexpr uint32_t id_s1 = idesc_bf16_f32(128, 64, true, true);      // B^T (MN) x one term of diag(w) X (MN)
-            constexpr uint32_t id_s2 = idesc_bf16_f32(128, 128, true, true);     // B^T (MN) x two terms
+            constexpr uint32_t id_s = idesc_bf16_f32(128, 192, true, true);      // B^T (MN) x the terms of diag(w) X (MN)
             constexpr uint32_t id_g = idesc_bf16_f32(128, 128, false, false);    // C (K) x B (K)
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);      // C (K) x H (MN); M (K) x X (MN)
             // descriptors of the fixed buffers and of ring and x slot 0: another slot,
@@ -490,29 +495,32 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     tc_fence_after();
                     const uint64_t dB = mn + ((S::ring + slot_b(nS) * 2 * kSlab + hf * kHalf) >> 4);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        mma_bf16_ss(tS(nS), dB + step_mn(q), d_xw + (xwbuf(hf) >> 4) + step_mn(q), id_s2, q ? 1u : hf);
-                        mma_bf16_ss(tS(nS) + 64, dB + step_mn(q), d_xw + ((xwbuf(hf) + 2 * kHalf) >> 4) + step_mn(q), id_s1, 1u);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        mma_bf16_ss(tS(nS), dB + step_mn(q), d_xw + (xwbuf(hf) >> 4) + step_mn(q), id_s, q ? 1u : hf);
                     mma_commit(bar(B_S_READY + hf));
                     // B goes free with the second of its two readers, S and G
                     if (hf && (STATE || nG > nS)) mma_commit(bar(B_RING_EMPTY + slot_b(nS)));
                     ++mS;
                     moved = true;
                 } else if (!STATE) {
-                    // Y(n) = M X and Yo(n) = C H; where the sequence ends in the tile, once group C
-                    // has zeroed what is behind it in x
+                    // Y(n) = M X + C (half H); where the sequence ends in the tile, once group C has
+                    // zeroed what is behind it in x; past the one-factor mask C H goes to Yo, once
+                    // that of the tile before is read
                     if (nY < nG && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1) &&
-                        (2 * nY + 1 < mS || !(sm.info[nY % kVec].flags & kPartial))) {
+                        (2 * nY + 1 < mS || !(sm.info[nY % kVec].flags & kPartial)) &&
+                        (nY == 0 || (sm.info[nY % kVec].flags & kOneFactor) ||
+                         mbar_test(bar(B_G_FREE + ((nY - 1) & 1)), ((nY - 1) >> 1) & 1))) {
                         tc_fence_after();
                         const uint64_t dX = mn + (xslot(nY) >> 4), dC = kmaj + ((S::ring + slot_c(nY) * 2 * kSlab) >> 4);
                         const uint32_t dm = tG(nY), dy = tY(nY);
 #pragma unroll
                         for (int q = 0; q < kTile / 16; ++q) mma_bf16_ts(dy, dm + 8 * q, dX + step_mn(q), id_o, q > 0);
-                        if (!(sm.info[nY % kVec].flags & kZeroStart)) {
+                        const int flags = sm.info[nY % kVec].flags;
+                        if (!(flags & kZeroStart)) {
+                            const uint32_t d = flags & kOneFactor ? dy : tYo, add = flags & kOneFactor ? 1u : 0u;
 #pragma unroll
                             for (int q = 0; q < N / 16; ++q)
-                                mma_bf16_ss(dm + 64, dC + step_k(q), d_h + step_mn(q), id_o, q > 0);
+                                mma_bf16_ss(d, dC + step_k(q), d_h + step_mn(q), id_o, q ? 1u : add);
                         }
                         mma_commit(bar(B_Y_READY + (nY & 1)));
                         mma_commit(bar(B_RING_EMPTY + slot_c(nY)));
@@ -635,6 +643,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (lane == 0) {
                 I.b = b0; I.h = h0; I.hu = hu0; I.t0 = t00; I.len = len0; I.flags = flags0;
                 I.decay = expf(all);
+                I.half = one ? __expf(0.5f * all) : 1.f;
                 I.D = D0;
             }
             __syncwarp();
@@ -704,14 +713,15 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t sv[2][8];
+                    uint32_t sv[3][8];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) tmem_ld8(tS(n - 1) + 64 * k + lane_off + q * 8, sv[k]);
+                    for (int k = 0; k < 3; ++k) tmem_ld8(tS(n - 1) + 64 * k + lane_off + q * 8, sv[k]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         H[q * 4 + j] = fma2(pair_of(decay, decay), H[q * 4 + j],
-                                            add2(pair_of(sv[0][2 * j], sv[0][2 * j + 1]), pair_of(sv[1][2 * j], sv[1][2 * j + 1])));
+                                            add2(pair_of(sv[0][2 * j], sv[0][2 * j + 1]),
+                                                 add2(pair_of(sv[1][2 * j], sv[1][2 * j + 1]), pair_of(sv[2][2 * j], sv[2][2 * j + 1]))));
                 }
                 tc_fence_before();
             };
@@ -796,10 +806,12 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 // C H of the tile before has read the buffer
                 if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
                 if (row < N && !(flags & kZeroStart)) {
+                    const pair_t half = pair_of(I.half, I.half);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, 4 * ph + c)) =
-                            make_uint4(bf16_of(H[4 * c]), bf16_of(H[4 * c + 1]), bf16_of(H[4 * c + 2]), bf16_of(H[4 * c + 3]));
+                            make_uint4(bf16_of(mul2(half, H[4 * c])), bf16_of(mul2(half, H[4 * c + 1])),
+                                       bf16_of(mul2(half, H[4 * c + 2])), bf16_of(mul2(half, H[4 * c + 3])));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -882,8 +894,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (row == 0) mbar_arrive(bar(B_M_READY + nb));
             // ---------------- the output
             const int t = I.t0 + row;
-            const bool zs = I.flags & kZeroStart;
-            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = zs ? 0.f : __expf(my_a), D = I.D;
+            const bool own = !one && !(I.flags & kZeroStart);       // C H comes by itself, with the row's decay
+            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a), D = I.D;
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
             const bool keep = t < I.len, inside = t < p.L, partial = I.flags & kPartial;
             const pair_t rf2 = pair_of(rf, rf), e2 = pair_of(e, e), D2 = pair_of(D, D);
@@ -891,38 +903,41 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mbar_wait_ool(bar(B_Y_READY + nb), par, abort_flag, p.status, 932);
             tc_fence_after();
             const bool store = inside && !*abort_flag;
-            auto load = [&](int q, uint32_t (&yv)[16], uint32_t (&ov)[16]) {
-                tmem_ld16(tY(n) + lane_off + q * 16, yv);
-                if (!zs) tmem_ld16(tg + 64 + q * 16, ov);
-            };
-            auto emit = [&](int q, const uint32_t (&yv)[16], const uint32_t (&ov)[16]) {
+            auto emit = [&](int q, const uint32_t (&yv)[16]) {
                 uint32_t o8[8];
                 uint4 xv[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) xv[c] = *reinterpret_cast<const uint4 *>(xt + sw128_offset(row, q * 2 + c));
                 const uint32_t *xu = reinterpret_cast<const uint32_t *>(xv);
+                if (own) {
+                    uint32_t ov[16];
+                    tmem_ld16(tYo + lane_off + q * 16, ov);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]),
-                                         fma2(e2, pair_of(ov[2 * c], ov[2 * c + 1]), mul2(D2, wide_of(xu[c])))));
+                    for (int c = 0; c < 8; ++c)
+                        o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]),
+                                             fma2(e2, pair_of(ov[2 * c], ov[2 * c + 1]), mul2(D2, wide_of(xu[c])))));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]), mul2(D2, wide_of(xu[c]))));
+                }
                 if (partial && !keep) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c) o8[c] = 0u;
                 }
                 if (store) store32(dst + q * 16, o8, whole);
             };
-            uint32_t ya[16], oa[16], yb[16], ob[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) oa[c] = ob[c] = 0u;      // stay zero where nothing enters the tile
-            load(0, ya, oa);
+            uint32_t ya[16], yb[16];
+            tmem_ld16(tY(n) + lane_off, ya);
             tmem_wait_ld();
 #pragma unroll 1
             for (int q = 0; q < 4; q += 2) {
-                load(q + 1, yb, ob);
-                emit(q, ya, oa);
+                tmem_ld16(tY(n) + lane_off + q * 16 + 16, yb);
+                emit(q, ya);
                 tmem_wait_ld();
-                if (q == 0) load(2, ya, oa);
-                emit(q + 1, yb, ob);
+                if (q == 0) tmem_ld16(tY(n) + lane_off + 32, ya);
+                emit(q + 1, yb);
                 tmem_wait_ld();
             }
             tc_fence_before();
