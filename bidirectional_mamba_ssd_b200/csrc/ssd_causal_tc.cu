@@ -14,8 +14,10 @@
 // so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, C H is taken of
 // exp(a_r) H, both add up in one accumulator, and the row's factor exp(a_t - a_r) is
 // applied to the fp32 sum. The factors stay within e^+-60 while the tile's decay is
-// at most 120; past that (a test on the tile) each entry of M takes its own
-// exponential and C H its own accumulator.
+// at most 120. Past that (a test on the tile) the columns are split at the last
+// token e of each block of 32 instead, exp(a_t - a_e) * exp(a_e - a_s), with a factor
+// per row and block, up to a decay of 80 in a block, and past that each entry of M
+// takes its own exponential; C H then has an accumulator of its own.
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
 // products whose result is rounded to bf16 (relative 2^-9 a term, random). The
@@ -67,6 +69,7 @@ constexpr int kStateThreads = 384;    // without the output groups
 constexpr int kVec = 4;               // tiles whose decays are kept
 constexpr uint32_t kHalf = 8192;      // 64 rows x 128 bytes
 constexpr float kMaxSpan = 120.f;     // decay of a tile up to which its mask is one factor per column
+constexpr float kMaxBlock = 80.f;     // decay of 32 tokens up to which it is one per column and one per row and block
 
 // A run of work of one CTA: n units from u0 on, of each the tiles [k0, k1) (k1 < 0:
 // all). from_cut: the state entering comes from the CTA before; to_cut: the state
@@ -149,15 +152,26 @@ __device__ void make_stages(const TcParams &p, int c, int nc, Stage *stages, int
         for (int b = b0; b < b1; ++b) mine += tiles_of(p, b);
         part[tid] = mine;
         __syncthreads();
-        if (tid == 0) {
-            long long acc = 0;
-            for (int i = 0; i < nth; ++i) {
-                const long long v = part[i];
-                part[i] = acc;
+        if (tid < 32) {
+            const int each = nth / 32;         // blocks are whole warps
+            long long own = 0;
+            for (int i = 0; i < each; ++i) own += part[tid * each + i];
+            long long acc = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, acc, o);
+                if (tid >= o) acc += up;
+            }
+            if (tid == 31) {
+                *total = acc * p.HU;
+                at[0] = at[1] = Place{p.batch * p.HU, 0};
+            }
+            acc -= own;
+            for (int i = 0; i < each; ++i) {
+                const long long v = part[tid * each + i];
+                part[tid * each + i] = acc;
                 acc += v;
             }
-            *total = acc * p.HU;
-            at[0] = at[1] = Place{p.batch * p.HU, 0};
         }
         __syncthreads();
         T = *total;
@@ -270,9 +284,9 @@ enum {
 };
 
 // What is known of a tile, from warp 2 to the other warps: a_s, the column
-// factors of M (the step sizes where each entry takes its own exponential), the
-// weights in the state.
-enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64 };
+// factors of M (dt_s times the decay from the token to the reference, if there is
+// one), the weights in the state.
+enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64, kBlocks = 128 };
 struct alignas(16) TileInfo {
     float a[kTile], col[kTile], w[kTile];
     int b, h, hu, t0, len, flags;
@@ -629,9 +643,19 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (one) flags0 |= kOneFactor;
             float a4[4], c4[4], w4[4];
 #pragma unroll
+            for (int i = 0; i < 4; ++i) a4[i] = A0 * ((lane ? ahead : 0.f) + up[i]);
+            // the reference of the columns: half the tile's decay, or the end of their block
+            float ref = 0.5f * all;
+            bool factor = one;
+            if (!one) {
+                const float first = __shfl_sync(0xffffffffu, a4[0], lane & ~7);
+                ref = __shfl_sync(0xffffffffu, a4[3], lane | 7);
+                factor = __all_sync(0xffffffffu, first - ref < kMaxBlock);
+                if (factor) flags0 |= kBlocks;
+            }
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a4[i] = A0 * ((lane ? ahead : 0.f) + up[i]);
-                c4[i] = one ? __expf(0.5f * all - a4[i]) * v[i] : v[i];
+                c4[i] = factor ? __expf(ref - a4[i]) * v[i] : v[i];
                 w4[i] = expf(A0 * ((lane < 31 ? behind : 0.f) + down[i])) * v[i];
             }
             const uint32_t vb = n % kVec;
@@ -839,7 +863,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 930);
             const TileInfo &I = sm.info[n % kVec];
             const float my_a = I.a[row], all = I.a[kTile - 1];
-            const bool one = I.flags & kOneFactor;
+            const bool one = I.flags & kOneFactor, blocks = I.flags & kBlocks;
             mbar_wait_ool(bar(B_G_READY + nb), par, abort_flag, p.status, 931);
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
@@ -852,6 +876,15 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                         const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
                         m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(f.x, f.y)));
                         m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), pair_of(f.z, f.w)));
+                    }
+                } else if (blocks) {
+                    const float r = __expf(my_a - I.a[(16 * c) | 31]);
+                    const pair_t rr = pair_of(r, r);
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
+                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), mul2(rr, pair_of(f.x, f.y))));
+                        m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), mul2(rr, pair_of(f.z, f.w))));
                     }
                 } else {
 #pragma unroll
@@ -965,6 +998,7 @@ __global__ void __launch_bounds__(256) causal_chain_kernel(const TcParams p, int
     constexpr int kParts = 64 * N / 1024;
     constexpr size_t kState = 64 * N / 4;
     const int c0 = blockIdx.x / kParts, e = (blockIdx.x % kParts) * 256 + threadIdx.x;
+    grid_launch_dependents();
     const int2 first = p.link[c0];
     if (first.x != kLinkFirst) return;
     const int u = first.y, b = u / p.HU;
@@ -1002,10 +1036,15 @@ __global__ void __launch_bounds__(256) causal_chain_kernel(const TcParams p, int
     }
 }
 
-// Rows of a ragged or paged batch: resolved pages, effective lengths (-1: skipped)
-// and the zeros of the output rows that no tile covers. Block (b, part).
-__global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, int *rows, int *lens) {
+// What the scan needs ahead of it: its flags cleared and, for a ragged or paged batch
+// (rows not nullptr), resolved pages, effective lengths (-1: skipped) and the zeros of
+// the output rows that no tile covers. Block (b, part).
+__global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, int *rows, int *lens, unsigned int *flags, int nflags) {
     const int b = blockIdx.x;
+    grid_launch_dependents();
+    if (b == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < nflags; i += 128) flags[i] = 0u;
+    if (!rows) return;
     int row = b;
     bool bad = false;
     if (a.slots) {
@@ -1063,14 +1102,24 @@ bool map_rows(CUtensorMap *m, const void *base, int inner, int count, int L, int
 
 template <int N, bool STATE>
 cudaError_t launch_tc(const CUtensorMap &x, const CUtensorMap &b, const CUtensorMap &c, const TcParams &p, int ctas,
-                      cudaStream_t stream) {
+                      bool follows, cudaStream_t stream) {
     auto k = causal_tc_kernel<N, STATE>;
     const size_t smem = Layout<N, STATE>::small + sizeof(Small) + 1024;
     static_assert(Layout<N, STATE>::small + sizeof(Small) + 1024 <= 232448, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k<<<ctas, STATE ? kStateThreads : kThreads, smem, stream>>>(x, b, c, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(STATE ? kStateThreads : kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // behind a kernel of this call the prologue overlaps that kernel's end
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, x, b, c, p);
 }
 
 template <int N>
@@ -1093,38 +1142,38 @@ cudaError_t run_tc(const CausalArgs &a, void *scratch, cudaStream_t stream) {
     p.status = a.status;
     p.batch = a.batch; p.L = a.L; p.H = a.H;
     p.halves = a.P / 64; p.HU = a.H * p.halves; p.heads_per_group = a.H / a.G;
-    if (a.seqlens || a.slots) {
-        int *rows = reinterpret_cast<int *>(ws + t.rows), *lens = reinterpret_cast<int *>(ws + t.lens);
-        // enough blocks a row to zero a long tail, few where the rows are many
-        const int parts = 8 * sms / a.batch;
-        causal_rows_kernel<<<dim3(a.batch, parts < 1 ? 1 : parts > 64 ? 64 : parts), 128, 0, stream>>>(a, rows, lens);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        p.rows = rows;
-        p.lens = lens;
-    }
     CUtensorMap tx, tb, tc;
     if (!map_rows(&tx, a.x, 64, p.HU, a.L, a.batch, a.x_st, a.x_sb) ||
         !map_rows(&tb, a.B, N, a.G, a.L, a.batch, a.b_st, a.b_sb) || !map_rows(&tc, a.C, N, a.G, a.L, a.batch, a.c_st, a.c_sb))
         return cudaErrorInvalidValue;
     const long long units = (long long)a.batch * p.HU, nt = (a.L + kTile - 1) / kTile;
-    if (units >= sms) {
-        p.order = kOrderHandoff;
-        if ((e = cudaMemsetAsync(p.flags, 0, sizeof(int) * (size_t)sms, stream)) != cudaSuccess) return e;
-        return launch_tc<N, false>(tx, tb, tc, p, sms, stream);
-    }
     // fewer units than SMs: the cut work costs a second pass over x and B and two
     // more launches, but spreads over every SM
     const long long share = (units * nt + sms - 1) / sms;
-    if (10 * nt > 16 * share + 60) {
-        p.order = kOrderState;
-        if ((e = launch_tc<N, true>(tx, tb, tc, p, sms, stream)) != cudaSuccess) return e;
+    p.order = units >= sms ? kOrderHandoff : 10 * nt > 16 * share + 60 ? kOrderNatural : kOrderWhole;
+    const bool ragged = a.seqlens || a.slots, first = ragged || p.order == kOrderHandoff;
+    if (first) {
+        int *rows = reinterpret_cast<int *>(ws + t.rows), *lens = reinterpret_cast<int *>(ws + t.lens);
+        if (ragged) {
+            p.rows = rows;
+            p.lens = lens;
+        }
+        // enough blocks a row to zero a long tail, few where the rows are many
+        const int parts = 8 * sms / a.batch;
+        const dim3 grid(ragged ? a.batch : 1, !a.seqlens && !a.slots ? 1 : parts < 1 ? 1 : parts > 64 ? 64 : parts);
+        causal_rows_kernel<<<grid, 128, 0, stream>>>(a, ragged ? rows : nullptr, lens, p.flags,
+                                                     p.order == kOrderHandoff ? sms : 0);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (p.order == kOrderNatural) {
+        TcParams st = p;
+        st.order = kOrderState;
+        if ((e = launch_tc<N, true>(tx, tb, tc, st, sms, first, stream)) != cudaSuccess) return e;
         causal_chain_kernel<N><<<sms * (64 * N / 1024), 256, 0, stream>>>(p, sms);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        p.order = kOrderNatural;
-        return launch_tc<N, false>(tx, tb, tc, p, sms, stream);
+        return launch_tc<N, false>(tx, tb, tc, p, sms, true, stream);
     }
-    p.order = kOrderWhole;
-    return launch_tc<N, false>(tx, tb, tc, p, (int)units, stream);
+    return launch_tc<N, false>(tx, tb, tc, p, p.order == kOrderWhole ? (int)units : sms, first, stream);
 }
 
 }  // namespace

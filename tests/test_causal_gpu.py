@@ -222,6 +222,23 @@ def test_fwd_strong_and_no_decay(ssd):
                 check_state(h[:, k], oh[:, k], f"{io} head {k}")
 
 
+def test_fwd_decay_ranges(ssd):
+    """Step sizes of 0.1 throughout: a tile of 128 tokens decays by e^-64, e^-115, e^-154, e^-218, e^-333, e^-512
+    (both sides of the spans where the masked matrix changes its reference), with start states."""
+    A = torch.tensor([-5.0, -9.0, -12.0, -17.0, -26.0, -40.0], device="cuda")
+    d = inputs((1, 300), 6, 64, 128, 2, "bf16", seed=12)
+    d["dt"].fill_(0.1)
+    h0 = torch.randn(1, 6, 64, 128, generator=d["g"], device="cuda")
+    o, oh = ref.fwd(d["x"], sizes(d), A, d["B"], d["C"], d["D"], h0, [300])
+    y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], A, d["B"], d["C"], d["D"], h0)
+    torch.cuda.synchronize()
+    assert ssd.ssd_get_device_status() == 0
+    for k in range(6):
+        check_out(y[:, :, k], o[:, :, k], "bf16", f"A {A[k].item()}")
+        check_out(y[:, :1, k], o[:, :1, k], "bf16", f"first token, A {A[k].item()}")
+        check_state(h[:, k], oh[:, k], f"A {A[k].item()}")
+
+
 STEPS = [(1, 4, 64, 128, 4, "bf16", False, False), (7, 2, 64, 64, 1, "bf16", True, True), (33, 8, 128, 128, 2, "bf16", False, True),
          (300, 4, 64, 128, 1, "bf16", True, False), (5, 3, 64, 64, 3, "f32", False, False), (130, 12, 192, 128, 4, "f32", True, True)]
 
