@@ -33,9 +33,9 @@
 // every part's own end state, a small kernel chains them, and the outputs follow.
 //
 // Roles (640 threads): warp 0 TMA producer; warp 1 MMA issuer, which polls what
-// is ready (S, then Y and Yo, then G) instead of waiting in a fixed order; warp 2
-// the decays of the coming tiles (up to four ahead) and what else is to be known
-// of them; warps 4..11 group C: diag(w) X by halves of a tile, and the state,
+// is ready (S, then Y and Yo, then G) instead of waiting in a fixed order; warps 2
+// and 3 the decays of the coming even and odd tiles (up to four ahead) and what else
+// is to be known of them; warps 4..11 group C: diag(w) X by halves of a tile, and the state,
 // rows n of it a thread, 32 columns each; warps 12..15 and 16..19 groups A and B:
 // mask and output of the even and the odd tiles, so that one tile's mask overlaps
 // the other's products and output; thread r owns tile row r.
@@ -274,8 +274,8 @@ enum {
     B_M_READY = 18,      // 2: output groups -> MMA: M of the tile
     B_Y_READY = 20,      // 2: MMA -> output groups and C: Y and Yo of the tile
     B_G_FREE = 22,       // 2: output groups -> MMA: the tile's TMEM buffers are read
-    B_VEC_READY = 24,    // kVec: warp 2 -> C and the output groups
-    B_VEC_FREE = 28,     // kVec: C and the output groups -> warp 2
+    B_VEC_READY = 24,    // kVec: warps 2, 3 -> C and the output groups
+    B_VEC_FREE = 28,     // kVec: C and the output groups -> warps 2, 3
     B_XW_READY = 32,     // 2: C -> MMA: a half of diag(w) X of the tile
     B_S_READY = 34,      // 2: MMA -> C: S of that half (and all before it)
     B_H_READY = 36,      // C -> MMA
@@ -283,7 +283,7 @@ enum {
     B_COUNT
 };
 
-// What is known of a tile, from warp 2 to the other warps: a_s, the column
+// What is known of a tile, from warps 2 and 3 to the others: a_s, the column
 // factors of M (dt_s times the decay from the token to the reference, if there is
 // one), the weights in the state.
 enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64, kBlocks = 128 };
@@ -573,14 +573,14 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mma_commit(bar(B_DONE));
             mbar_drain(bar(B_DONE), 0);
         }
-    } else if (warp == 2) {
+    } else if (warp < 4) {
         // ------------------------------------------------------------ decays of the coming tiles
         // (lane l: tokens 4 l .. 4 l + 3 of the tile)
         Walk w(p, sm.stages);
         uint32_t raw[4] = {0u, 0u, 0u, 0u};
         float A = 0.f, D = 0.f, bias = 0.f;
         auto load = [&](bool there) {
-            if (there && w.first) {
+            if (there) {
                 A = p.A[w.h];
                 D = !STATE && p.D ? p.D[w.h] : 0.f;
                 bias = p.step.bias ? p.step.bias[w.h] : 0.f;
@@ -599,7 +599,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         float A_ = 0.f, D_ = 0.f, bias_ = 0.f;
         bool there = false;
 #pragma unroll 1
-        for (uint32_t n = 0;;) {
+        for (uint32_t n = warp & 1;;) {
             float v[4], up[4], down[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = t0 + 4 * lane + i < len ? p.step.with(bf2f(raw[i]), bias_) : 0.f;
@@ -608,7 +608,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const float A0 = A_, D0 = D_;
             const bool had = there;
             // the next tile's step sizes are on their way meanwhile
-            there = w.next();
+            there = true;
+            for (int i = had || (warp & 1) ? 2 : 1; there && i > 0; --i) there = w.next();
             load(there);
             if (there) {
                 const Stage &st = sm.stages[w.s];
@@ -672,7 +673,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_VEC_READY + vb));
-            ++n;
+            n += 2;
             if (!there) break;
         }
     } else if (warp >= 4 && warp < 12) {
