@@ -9,15 +9,15 @@
 // Four products a tile: G = C B^T, Y = M X with M = G c_s under the causal mask,
 // Yo = C H, S = B^T diag(w) X.
 //
-// The decay between two tokens is split at the tile's half decay a_r = a_T / 2:
+// The decay between two tokens is split at a reference a_r:
 //   exp(a_t - a_s) = exp(a_t - a_r) * exp(a_r - a_s)
-// so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, C H is taken of
-// exp(a_r) H, both add up in one accumulator, and the row's factor exp(a_t - a_r) is
-// applied to the fp32 sum. The factors stay within e^+-60 while the tile's decay is
-// at most 120. Past that (a test on the tile) the columns are split at the last
-// token e of each block of 32 instead, exp(a_t - a_e) * exp(a_e - a_s), with a factor
-// per row and block, up to a decay of 80 in a block, and past that each entry of M
-// takes its own exponential; C H then has an accumulator of its own.
+// so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, and the row's
+// factor exp(a_t - a_r) is applied to the fp32 result. With a_r half the tile's decay
+// both stay within e^+-75 while that is at most 150; C H is taken of exp(a_r) H and
+// adds up with M X in one accumulator. Past that (a test on the tile) the rows of each
+// half of the tile have a reference of their own, half way through their half, and the
+// columns a factor for each, up to a decay of 150 in a half; past that each entry takes
+// its own exponential. In both C H has an accumulator of its own.
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
 // products whose result is rounded to bf16 (relative 2^-9 a term, random). The
@@ -68,8 +68,7 @@ constexpr int kThreads = 640;
 constexpr int kStateThreads = 384;    // without the output groups
 constexpr int kVec = 4;               // tiles whose decays are kept
 constexpr uint32_t kHalf = 8192;      // 64 rows x 128 bytes
-constexpr float kMaxSpan = 120.f;     // decay of a tile up to which its mask is one factor per column
-constexpr float kMaxBlock = 80.f;     // decay of 32 tokens up to which it is one per column and one per row and block
+constexpr float kMaxSpan = 150.f;     // decay up to which a tile's, or a half tile's, mask has one factor per column
 
 // A run of work of one CTA: n units from u0 on, of each the tiles [k0, k1) (k1 < 0:
 // all). from_cut: the state entering comes from the CTA before; to_cut: the state
@@ -286,10 +285,11 @@ enum {
 // What is known of a tile, from warps 2 and 3 to the others: a_s, the column
 // factors of M (dt_s times the decay from the token to the reference, if there is
 // one), the weights in the state.
-enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64, kBlocks = 128 };
+enum { kZeroStart = 1, kFirst = 2, kLast = 4, kFromCut = 8, kToCut = 16, kOneFactor = 32, kPartial = 64, kHalves = 128 };
 struct alignas(16) TileInfo {
-    float a[kTile], col[kTile], w[kTile];
+    float a[kTile], col[2][kTile], w[kTile];     // col: for the rows of either half
     int b, h, hu, t0, len, flags;
+    float ref[2];           // a_r of either half's rows
     float decay, half, D;   // exp(a_T); the factor of H in C H: exp(a_r), or 1; the head's skip factor
 };
 
@@ -645,30 +645,30 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             float a4[4], c4[4], w4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) a4[i] = A0 * ((lane ? ahead : 0.f) + up[i]);
-            // the reference of the columns: half the tile's decay, or the end of their block
-            float ref = 0.5f * all;
-            bool factor = one;
-            if (!one) {
-                const float first = __shfl_sync(0xffffffffu, a4[0], lane & ~7);
-                ref = __shfl_sync(0xffffffffu, a4[3], lane | 7);
-                factor = __all_sync(0xffffffffu, first - ref < kMaxBlock);
-                if (factor) flags0 |= kBlocks;
-            }
+            const float mid = __shfl_sync(0xffffffffu, a4[3], 15);
+            const bool halves = !one && mid > -kMaxSpan && all - mid > -kMaxSpan, factor = one || halves;
+            if (halves) flags0 |= kHalves;
+            const float ref0 = one ? 0.5f * all : 0.5f * mid, ref1 = one ? ref0 : 0.5f * (mid + all);
+            float d4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                c4[i] = factor ? __expf(ref - a4[i]) * v[i] : v[i];
+                c4[i] = factor ? __expf(ref0 - a4[i]) * v[i] : v[i];
+                d4[i] = one ? c4[i] : factor ? __expf(ref1 - a4[i]) * v[i] : v[i];
                 w4[i] = expf(A0 * ((lane < 31 ? behind : 0.f) + down[i])) * v[i];
             }
             const uint32_t vb = n % kVec;
             if (n >= kVec) mbar_wait_ool(bar(B_VEC_FREE + vb), ((n / kVec) - 1) & 1, abort_flag, p.status, 920);
             TileInfo &I = sm.info[vb];
             reinterpret_cast<float4 *>(I.a)[lane] = make_float4(a4[0], a4[1], a4[2], a4[3]);
-            reinterpret_cast<float4 *>(I.col)[lane] = make_float4(c4[0], c4[1], c4[2], c4[3]);
+            reinterpret_cast<float4 *>(I.col[0])[lane] = make_float4(c4[0], c4[1], c4[2], c4[3]);
+            reinterpret_cast<float4 *>(I.col[1])[lane] = make_float4(d4[0], d4[1], d4[2], d4[3]);
             reinterpret_cast<float4 *>(I.w)[lane] = make_float4(w4[0], w4[1], w4[2], w4[3]);
             if (lane == 0) {
                 I.b = b0; I.h = h0; I.hu = hu0; I.t0 = t00; I.len = len0; I.flags = flags0;
                 I.decay = expf(all);
-                I.half = one ? __expf(0.5f * all) : 1.f;
+                I.half = one ? __expf(ref0) : 1.f;
+                I.ref[0] = ref0;
+                I.ref[1] = ref1;
                 I.D = D0;
             }
             __syncwarp();
@@ -863,35 +863,26 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // TMEM meanwhile; columns [16 c, 16 c + 16) of M are 8 words over G columns already read
             mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 930);
             const TileInfo &I = sm.info[n % kVec];
-            const float my_a = I.a[row], all = I.a[kTile - 1];
-            const bool one = I.flags & kOneFactor, blocks = I.flags & kBlocks;
+            const float my_a = I.a[row], *col = I.col[wq >> 1];
+            const bool one = I.flags & kOneFactor, factor = I.flags & (kOneFactor | kHalves);
             mbar_wait_ool(bar(B_G_READY + nb), par, abort_flag, p.status, 931);
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
             const int chunks = 2 * wq + 2;             // up to and with the diagonal
             auto mask = [&](int c, const uint32_t (&gv)[16]) {
                 uint32_t m[8];
-                if (one) {
+                if (factor) {
 #pragma unroll
                     for (int q = 0; q < 16; q += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
+                        const float4 f = *reinterpret_cast<const float4 *>(col + 16 * c + q);
                         m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(f.x, f.y)));
                         m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), pair_of(f.z, f.w)));
-                    }
-                } else if (blocks) {
-                    const float r = __expf(my_a - I.a[(16 * c) | 31]);
-                    const pair_t rr = pair_of(r, r);
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&I.col[16 * c + q]);
-                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), mul2(rr, pair_of(f.x, f.y))));
-                        m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), mul2(rr, pair_of(f.z, f.w))));
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 16; q += 2) {
-                        const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * I.col[16 * c + q];
-                        const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * I.col[16 * c + q + 1];
+                        const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * col[16 * c + q];
+                        const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * col[16 * c + q + 1];
                         m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(e0, e1)));
                     }
                 }
@@ -929,7 +920,7 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // ---------------- the output
             const int t = I.t0 + row;
             const bool own = !one && !(I.flags & kZeroStart);       // C H comes by itself, with the row's decay
-            const float rf = one ? __expf(my_a - 0.5f * all) : 1.f, e = __expf(my_a), D = I.D;
+            const float rf = factor ? __expf(my_a - I.ref[wq >> 1]) : 1.f, e = __expf(my_a), D = I.D;
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
             const bool keep = t < I.len, inside = t < p.L, partial = I.flags & kPartial;
             const pair_t rf2 = pair_of(rf, rf), e2 = pair_of(e, e), D2 = pair_of(D, D);

@@ -223,9 +223,9 @@ def test_fwd_strong_and_no_decay(ssd):
 
 
 def test_fwd_decay_ranges(ssd):
-    """Step sizes of 0.1 throughout: a tile of 128 tokens decays by e^-64, e^-115, e^-154, e^-218, e^-333, e^-512
-    (both sides of the spans where the masked matrix changes its reference), with start states."""
-    A = torch.tensor([-5.0, -9.0, -12.0, -17.0, -26.0, -40.0], device="cuda")
+    """Step sizes of 0.1 throughout: a tile of 128 tokens decays by e^-64, e^-147, e^-154, e^-282, e^-320, e^-512
+    (both sides of the spans where the masked matrix changes its references), with start states."""
+    A = torch.tensor([-5.0, -11.5, -12.0, -22.0, -25.0, -40.0], device="cuda")
     d = inputs((1, 300), 6, 64, 128, 2, "bf16", seed=12)
     d["dt"].fill_(0.1)
     h0 = torch.randn(1, 6, 64, 128, generator=d["g"], device="cuda")
