@@ -13,6 +13,7 @@ namespace ssd {
 // Step size of one token and head: as given, or from the raw projection as
 // min(max(softplus(raw + bias), lo), hi). Past u = 20 softplus(u) - u is below
 // e^-20 = 2^-28.9, less than half an ulp of u in fp32.
+static __device__ __noinline__ float softplus(float u) { return u > 20.f ? u : log1pf(expf(u)); }
 struct StepSize {
     const float *bias;   // (H) or nullptr: the step size is used as given
     float lo, hi;
@@ -22,9 +23,7 @@ struct StepSize {
     // the same with the head's bias at hand
     __device__ __forceinline__ float with(float v, float b) const {
         if (!bias) return v;
-        const float u = v + b;
-        const float s = u > 20.f ? u : log1pf(expf(u));
-        return fminf(fmaxf(s, lo), hi);
+        return fminf(fmaxf(softplus(v + b), lo), hi);
     }
 };
 

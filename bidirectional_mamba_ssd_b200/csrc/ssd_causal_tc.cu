@@ -694,12 +694,13 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         for (uint32_t n = 0; n <= nsteps; ++n) {
             const TileInfo &I = sm.info[n % kVec];
             const bool tile = n < nsteps;
-            int t0 = 0, len = 0;
+            int t0 = 0, len = 0, b = 0, hu = 0, flags = 0;
+            float this_decay = 0.f, half = 1.f;
             if (tile) {
                 mbar_wait_ool(bar(B_VEC_READY + n % kVec), (n / kVec) & 1, abort_flag, p.status, 921);
                 mbar_wait_ool(bar(B_X_FULL + slot_x(n)), use_x(n) & 1, abort_flag, p.status, 922);
-                t0 = I.t0;
-                len = I.len;
+                t0 = I.t0; len = I.len; b = I.b; hu = I.hu; flags = I.flags;
+                this_decay = I.decay; half = I.half;
             }
             // half of diag(w) X in three terms
             auto build = [&](int hf) {
@@ -750,19 +751,9 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 }
                 tc_fence_before();
             };
-            // one buffer for diag(w) X and one S: a half waits for the half before, and S is
-            // read ahead of the first. Two of each: a half waits for its like of the tile before.
-            if (n >= 1) mbar_wait_ool(bar(B_S_READY + !STATE), (n - 1) & 1, abort_flag, p.status, 924);
-            if (!STATE && n >= 1) advance();
-            if (tile) build(0);
-            if (STATE && n >= 1) {
-                mbar_wait_ool(bar(B_S_READY + 1), (n - 1) & 1, abort_flag, p.status, 928);
-                if (tile) build(1);
-                advance();
-            } else if (STATE && tile) {
-                build(1);
-            }
-            if (n >= 1) {
+            // the state behind the tile before goes where it is wanted; the one entering this
+            // tile, where a part begins with it, comes in
+            auto settle = [&]() {
                 if (pflags & kLast) {
                     // the state behind the unit or the part of it: the end state, or to the CTA
                     // behind (with kOrderNatural the chain has put it there)
@@ -791,52 +782,68 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                         }
                     }
                 }
-            }
-            if (!tile) break;
-            const int flags = I.flags;
-            if (flags & kFirst) {
-                all = 1.f;
-                const float *from = nullptr;
-                if (!STATE) {
-                    if (flags & kFromCut) {
-                        from = p.cut + (size_t)(blockIdx.x - 1) * 64 * N;
-                        if (p.order == kOrderHandoff) {
-                            if (cid == 0) flag_wait(p.flags + blockIdx.x - 1, 1u, abort_flag, p.status, 925);
-                            sync_state();
+                if (flags & kFirst) {
+                    all = 1.f;
+                    const float *from = nullptr;
+                    if (!STATE) {
+                        if (flags & kFromCut) {
+                            from = p.cut + (size_t)(blockIdx.x - 1) * 64 * N;
+                            if (p.order == kOrderHandoff) {
+                                if (cid == 0) flag_wait(p.flags + blockIdx.x - 1, 1u, abort_flag, p.status, 925);
+                                sync_state();
+                            }
+                        } else if (p.init && p.order == kOrderNatural && (flags & kToCut)) {
+                            from = p.start + (size_t)blockIdx.x * 64 * N;
+                        } else if (p.init) {
+                            from = p.init + ((size_t)(p.rows ? p.rows[b] : b) * p.HU + hu) * 64 * N;
                         }
-                    } else if (p.init && p.order == kOrderNatural && (flags & kToCut)) {
-                        from = p.start + (size_t)blockIdx.x * 64 * N;
-                    } else if (p.init) {
-                        from = p.init + ((size_t)(p.rows ? p.rows[I.b] : I.b) * p.HU + I.hu) * 64 * N;
+                    }
+                    if (from && row < N) {
+                        // another CTA of this launch may have written it: past L1
+                        from += 32 * ph * N + row;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) H[j] = pair_of(__ldcg(from + (2 * j) * N), __ldcg(from + (2 * j + 1) * N));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) H[j] = 0ull;
                     }
                 }
-                if (from && row < N) {
-                    // another CTA of this launch may have written it: past L1
-                    from += 32 * ph * N + row;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) H[j] = pair_of(__ldcg(from + (2 * j) * N), __ldcg(from + (2 * j + 1) * N));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) H[j] = 0ull;
+                decay = this_decay;
+                all *= decay;
+                pflags = flags;
+                pb = b;
+                phu = hu;
+            };
+            // one buffer for diag(w) X and one S: a half waits for the half before, and S is
+            // read ahead of the first. Two of each: a half waits for its like of the tile before.
+            // (One call site for each piece: the loop has to stay in the instruction cache.)
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                if (n >= 1 && (STATE || hf == 0))
+                    mbar_wait_ool(bar(B_S_READY + (STATE ? hf : 1)), (n - 1) & 1, abort_flag, p.status, 924);
+                if (!STATE && hf == 0 && n >= 1) advance();
+                if (!STATE && hf == 1) {
+                    settle();
+                    if (!tile) break;
+                    mbar_wait_ool(bar(B_S_READY), n & 1, abort_flag, p.status, 927);
                 }
+                if (tile) build(hf);
             }
-            decay = I.decay;
-            all *= decay;
-            pflags = flags;
-            pb = I.b;
-            phu = I.hu;
+            if (STATE) {
+                if (n >= 1) advance();
+                settle();
+            }
+            if (!tile) break;
             if (!STATE) {
-                mbar_wait_ool(bar(B_S_READY), n & 1, abort_flag, p.status, 927);
-                build(1);
                 // C H of the tile before has read the buffer
                 if (n >= 1) mbar_wait_ool(bar(B_Y_READY + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag, p.status, 926);
                 if (row < N && !(flags & kZeroStart)) {
-                    const pair_t half = pair_of(I.half, I.half);
+                    const pair_t f = pair_of(half, half);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         *reinterpret_cast<uint4 *>(g + S::h + sw128_offset(row, 4 * ph + c)) =
-                            make_uint4(bf16_of(mul2(half, H[4 * c])), bf16_of(mul2(half, H[4 * c + 1])),
-                                       bf16_of(mul2(half, H[4 * c + 2])), bf16_of(mul2(half, H[4 * c + 3])));
+                            make_uint4(bf16_of(mul2(f, H[4 * c])), bf16_of(mul2(f, H[4 * c + 1])),
+                                       bf16_of(mul2(f, H[4 * c + 2])), bf16_of(mul2(f, H[4 * c + 3])));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -869,42 +876,50 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
             const int chunks = 2 * wq + 2;             // up to and with the diagonal
-            auto mask = [&](int c, const uint32_t (&gv)[16]) {
-                uint32_t m[8];
-                if (factor) {
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(col + 16 * c + q);
-                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(f.x, f.y)));
-                        m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), pair_of(f.z, f.w)));
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 16; q += 2) {
-                        const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * col[16 * c + q];
-                        const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * col[16 * c + q + 1];
-                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(e0, e1)));
-                    }
-                }
+            // entries behind the row's own token are dropped, never multiplied
+            auto put = [&](int c, uint32_t (&m)[8]) {
                 if (c >= 2 * wq) {
-                    // entries behind the row's own token are dropped, never multiplied
                     const int own = row - 16 * c;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) m[q] = 2 * q + 1 <= own ? m[q] : 2 * q <= own ? (m[q] & 0xffffu) : 0u;
                 }
                 tmem_st8(tg + 8 * c, m);
             };
-            uint32_t ga[16], gb[16];
-            tmem_ld16(tg, ga);
-            tmem_wait_ld();
+            uint32_t ga[16], gb[16], m[8];
+            if (factor) {
+                auto mask = [&](int c, const uint32_t (&gv)[16]) {
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(col + 16 * c + q);
+                        m[q / 2] = bf16_of(mul2(pair_of(gv[q], gv[q + 1]), pair_of(f.x, f.y)));
+                        m[q / 2 + 1] = bf16_of(mul2(pair_of(gv[q + 2], gv[q + 3]), pair_of(f.z, f.w)));
+                    }
+                    put(c, m);
+                };
+                tmem_ld16(tg, ga);
+                tmem_wait_ld();
 #pragma unroll 1
-            for (int c = 0; c < chunks; c += 2) {
-                tmem_ld16(tg + 16 * c + 16, gb);
-                mask(c, ga);
-                tmem_wait_ld();
-                if (c + 2 < chunks) tmem_ld16(tg + 16 * c + 32, ga);
-                mask(c + 1, gb);
-                tmem_wait_ld();
+                for (int c = 0; c < chunks; c += 2) {
+                    tmem_ld16(tg + 16 * c + 16, gb);
+                    mask(c, ga);
+                    tmem_wait_ld();
+                    if (c + 2 < chunks) tmem_ld16(tg + 16 * c + 32, ga);
+                    mask(c + 1, gb);
+                    tmem_wait_ld();
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    tmem_ld16(tg + 16 * c, ga);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 16; q += 2) {
+                        const float e0 = __expf(fminf(my_a - I.a[16 * c + q], 0.f)) * col[16 * c + q];
+                        const float e1 = __expf(fminf(my_a - I.a[16 * c + q + 1], 0.f)) * col[16 * c + q + 1];
+                        m[q / 2] = bf16_of(mul2(pair_of(ga[q], ga[q + 1]), pair_of(e0, e1)));
+                    }
+                    put(c, m);
+                }
             }
 #pragma unroll 1
             for (int c = chunks; c < 8; c += 2) {
@@ -923,29 +938,23 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const float rf = factor ? __expf(my_a - I.ref[wq >> 1]) : 1.f, e = __expf(my_a), D = I.D;
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
             const bool keep = t < I.len, inside = t < p.L, partial = I.flags & kPartial;
-            const pair_t rf2 = pair_of(rf, rf), e2 = pair_of(e, e), D2 = pair_of(D, D);
+            const pair_t rf2 = pair_of(rf, rf), D2 = pair_of(D, D);
             const uint8_t *xt = g + xslot(n);
             mbar_wait_ool(bar(B_Y_READY + nb), par, abort_flag, p.status, 932);
             tc_fence_after();
             const bool store = inside && !*abort_flag;
-            auto emit = [&](int q, const uint32_t (&yv)[16]) {
+            // y = rf Y + D x (+ more), 16 columns
+            auto emit = [&](int q, const uint32_t (&yv)[16], const pair_t *more) {
                 uint32_t o8[8];
                 uint4 xv[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) xv[c] = *reinterpret_cast<const uint4 *>(xt + sw128_offset(row, q * 2 + c));
                 const uint32_t *xu = reinterpret_cast<const uint32_t *>(xv);
-                if (own) {
-                    uint32_t ov[16];
-                    tmem_ld16(tYo + lane_off + q * 16, ov);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]),
-                                             fma2(e2, pair_of(ov[2 * c], ov[2 * c + 1]), mul2(D2, wide_of(xu[c])))));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]), mul2(D2, wide_of(xu[c]))));
+                for (int c = 0; c < 8; ++c) {
+                    pair_t v = mul2(D2, wide_of(xu[c]));
+                    if (more) v = add2(v, more[c]);
+                    o8[c] = bf16_of(fma2(rf2, pair_of(yv[2 * c], yv[2 * c + 1]), v));
                 }
                 if (partial && !keep) {
 #pragma unroll
@@ -954,16 +963,30 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 if (store) store32(dst + q * 16, o8, whole);
             };
             uint32_t ya[16], yb[16];
-            tmem_ld16(tY(n) + lane_off, ya);
-            tmem_wait_ld();
+            if (!own) {
+                tmem_ld16(tY(n) + lane_off, ya);
+                tmem_wait_ld();
 #pragma unroll 1
-            for (int q = 0; q < 4; q += 2) {
-                tmem_ld16(tY(n) + lane_off + q * 16 + 16, yb);
-                emit(q, ya);
-                tmem_wait_ld();
-                if (q == 0) tmem_ld16(tY(n) + lane_off + 32, ya);
-                emit(q + 1, yb);
-                tmem_wait_ld();
+                for (int q = 0; q < 4; q += 2) {
+                    tmem_ld16(tY(n) + lane_off + q * 16 + 16, yb);
+                    emit(q, ya, nullptr);
+                    tmem_wait_ld();
+                    if (q == 0) tmem_ld16(tY(n) + lane_off + 32, ya);
+                    emit(q + 1, yb, nullptr);
+                    tmem_wait_ld();
+                }
+            } else {
+                const pair_t e2 = pair_of(e, e);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    pair_t more[8];
+                    tmem_ld16(tY(n) + lane_off + q * 16, ya);
+                    tmem_ld16(tYo + lane_off + q * 16, yb);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) more[c] = mul2(e2, pair_of(yb[2 * c], yb[2 * c + 1]));
+                    emit(q, ya, more);
+                }
             }
             tc_fence_before();
             sync_g();
