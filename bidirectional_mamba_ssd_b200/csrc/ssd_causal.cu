@@ -6,13 +6,13 @@
 //
 // The state's columns p do not depend on one another, so a CTA takes COLS of a
 // head's P columns and walks its tokens with that part of the state in
-// registers: a thread owns 4 p x 8 n, reads 16 operands a token from shared
-// memory for its 96 operations (packed two to an instruction, f32x2) and meets
-// the other n in a butterfly. Tokens arrive in chunks of kTok through
-// cp.async, two chunks deep. What bounds it: instruction issue (about 75 a
-// token and warp) with many units, the token chain's latency with few; there
-// the sequence is cut into segments (own end states, a carry, then the
-// outputs), which costs a second pass over x and B.
+// registers: a thread owns 4 p x 8 n, reads 20 operands a token from shared memory
+// for its 96 operations (packed two to an instruction, f32x2) and meets the other n in
+// a butterfly. Tokens arrive in chunks of kTok through cp.async, two chunks deep. What
+// bounds it: instruction issue with many units (64 x 500 tokens, 24 heads of 64, N =
+// 128: 581 us, where 2 p a thread take 706 us and 16 columns a CTA about as long), a
+// warp's own time per token with few; there the sequence is cut into segments (own
+// end states, a carry, then the outputs), which costs a second pass over x and B.
 #include <stdint.h>
 
 #include "ssd_causal.h"
@@ -22,6 +22,7 @@ namespace ssd {
 namespace {
 
 constexpr int kTok = 16;
+constexpr int KP = 4;       // columns of a thread
 
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {
@@ -67,16 +68,16 @@ struct SimtSmem {
 };
 
 template <typename T, int N, int COLS, int MODE>
-__global__ void __launch_bounds__(COLS *N / 32)
+__global__ void __launch_bounds__(COLS *N / (8 * KP))
 causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
-    constexpr int THREADS = COLS * N / 32;
+    constexpr int THREADS = COLS * N / (8 * KP);
     constexpr int NG = N / 8;                 // lanes that share a column
     constexpr bool OUT = MODE == kCausalOutput;
     using S = SimtSmem<T, N, COLS>;
     extern __shared__ __align__(16) uint8_t raw[];
     S &sm = *reinterpret_cast<S *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gn = lane % NG, cg = (warp * 32 + lane) / NG;   // n group, column group (4 columns)
+    const int gn = lane % NG, cg = (warp * 32 + lane) / NG;   // n group, column group (KP columns)
     const int parts = a.P / COLS;
     const int part = blockIdx.x % parts;
     const int seg = (blockIdx.x / parts) % sg.count;
@@ -105,14 +106,14 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     const T *dtp = static_cast<const T *>(a.dt) + (long long)b * a.dt_sb + h;
     const float A = a.A[h], D = OUT && a.D ? a.D[h] : 0.f;
 
-    // state: element (4 cg + k, n) with n = 4 gn + i (i < 4) and N / 2 + 4 gn + i
-    f32x2 H[4][4];
-    const size_t col = (size_t)part * COLS + 4 * cg;
+    // state: element (KP cg + k, n) with n = 4 gn + i (i < 4) and N / 2 + 4 gn + i
+    f32x2 H[KP][4];
+    const size_t col = (size_t)part * COLS + KP * cg;
     const float *start = nullptr;
     if (OUT && sg.count > 1) start = sg.state + (((size_t)bh * sg.count + seg) * a.P + col) * N;
     else if (OUT && a.init) start = a.init + (((size_t)row * a.H + h) * a.P + col) * N;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < KP; ++k)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -150,16 +151,16 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
         cp_wait();
         __syncthreads();      // chunk here; the other buffer is read by nobody
         if (t0 + kTok < end) fetch(t0 + kTok, buf ^ 1);
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < m; ++t) {
             const float2 gd = sm.gd[buf][t];
-            const float4 x = lds4(&sm.x[buf][t][4 * cg]);
+            const float4 x = lds4(&sm.x[buf][t][KP * cg]);
+            float xs[KP] = {x.x, x.y, x.z, x.w};
             const float4 b0 = lds4(&sm.B[buf][t][4 * gn]), b1 = lds4(&sm.B[buf][t][N / 2 + 4 * gn]);
             const f32x2 Bv[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
             const f32x2 G = pack2(gd.x, gd.x);
-            const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < KP; ++k) {
                 const float u = gd.y * xs[k];
                 const f32x2 U = pack2(u, u);
 #pragma unroll
@@ -168,26 +169,31 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
             if (OUT) {
                 const float4 c0 = lds4(&sm.C[buf][t][4 * gn]), c1 = lds4(&sm.C[buf][t][N / 2 + 4 * gn]);
                 const f32x2 Cv[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
-                float y[4];
+                float y[KP];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < KP; ++k) {
                     const f32x2 s = fma2(H[k][3], Cv[3], fma2(H[k][2], Cv[2], fma2(H[k][1], Cv[1], mul2(H[k][0], Cv[0]))));
                     const float2 f = unpack2(s);
                     y[k] = f.x + f.y;
                 }
-                // butterfly over the NG lanes of a column group: two steps halve the
+                // butterfly over the NG lanes of a column group: the first steps halve the
                 // columns a lane carries, the others add
-                const bool u1 = gn & (NG / 2), u2 = gn & (NG / 4);
-                const float r0 = (u1 ? y[2] : y[0]) + __shfl_xor_sync(0xffffffffu, u1 ? y[0] : y[2], NG / 2);
-                const float r1 = (u1 ? y[3] : y[1]) + __shfl_xor_sync(0xffffffffu, u1 ? y[1] : y[3], NG / 2);
-                float r = (u2 ? r1 : r0) + __shfl_xor_sync(0xffffffffu, u2 ? r0 : r1, NG / 4);
+                int keep = 0, o = NG / 2;
 #pragma unroll
-                for (int o = NG / 8; o >= 1; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-                if ((gn & (NG / 4 - 1)) == 0) {
-                    const int k = (u1 ? 2 : 0) + (u2 ? 1 : 0);
-                    const float xk = u1 ? (u2 ? x.w : x.z) : (u2 ? x.y : x.x);
-                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + 4 * cg + k, a.D ? fmaf(D, xk, r) : r);
+                for (int m = KP / 2; m >= 1; m >>= 1, o >>= 1) {
+                    const bool up = gn & o;
+#pragma unroll
+                    for (int k = 0; k < m; ++k) {
+                        const float send = up ? y[k] : y[k + m], mine = up ? y[k + m] : y[k];
+                        y[k] = mine + __shfl_xor_sync(0xffffffffu, send, o);
+                        xs[k] = up ? xs[k + m] : xs[k];
+                    }
+                    keep += up ? m : 0;
                 }
+#pragma unroll
+                for (; o >= 1; o >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+                if ((gn & (NG / KP - 1)) == 0)
+                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + KP * cg + keep, a.D ? fmaf(D, xs[0], y[0]) : y[0]);
             }
         }
     }
@@ -207,7 +213,7 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     }
     if (last) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < KP; ++k)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const float2 u = unpack2(H[k][2 * q]), v = unpack2(H[k][2 * q + 1]);
@@ -247,24 +253,35 @@ __global__ void __launch_bounds__(256) causal_carry_kernel(const CausalArgs a, c
     float4 *st = reinterpret_cast<float4 *>(sg.state) + bh * sg.count * per + e;
     const float *dc = sg.decay + bh * sg.count;
     // segments that start behind the sequence are never read
-    const int n = min(sg.count, (a.len(b) + sg.tokens - 1) / sg.tokens);
-    for (int g = 0; g < (n < 1 ? 1 : n); ++g) {
-        const float4 own = g + 1 < n ? st[(size_t)g * per] : s;
-        st[(size_t)g * per] = s;
-        if (g + 1 < n) {
-            const float d = dc[g];
-            s = make_float4(fmaf(d, s.x, own.x), fmaf(d, s.y, own.y), fmaf(d, s.z, own.z), fmaf(d, s.w, own.w));
-        }
+    const int n = max(1, min(sg.count, (a.len(b) + sg.tokens - 1) / sg.tokens));
+    constexpr int kAhead = 8;              // loads in flight
+    for (int g = 0; g < n; g += kAhead) {
+        float4 own[kAhead];
+        float d[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (g + q + 1 < n) {
+                own[q] = st[(size_t)(g + q) * per];
+                d[q] = dc[g + q];
+            }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (g + q < n) {
+                st[(size_t)(g + q) * per] = s;
+                if (g + q + 1 < n)
+                    s = make_float4(fmaf(d[q], s.x, own[q].x), fmaf(d[q], s.y, own[q].y), fmaf(d[q], s.z, own[q].z),
+                                    fmaf(d[q], s.w, own[q].w));
+            }
     }
 }
 
-constexpr int kCols = 16;   // columns of a CTA
+constexpr int kCols = 32;   // columns of a CTA
 
 template <typename T, int N>
 cudaError_t run_simt(const CausalArgs &a, const CausalSegments &s, int mode, cudaStream_t stream) {
     const long long grid = (long long)a.batch * a.H * s.count * (a.P / kCols);
     if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
-    const int threads = kCols * N / 32;
+    const int threads = kCols * N / (8 * KP);
     const size_t smem = sizeof(SimtSmem<T, N, kCols>);
     static_assert(sizeof(SimtSmem<T, N, kCols>) <= 48 * 1024, "shared memory within the default limit");
     if (mode == kCausalOutput) causal_simt_kernel<T, N, kCols, kCausalOutput><<<(unsigned)grid, threads, smem, stream>>>(a, s);
@@ -280,8 +297,8 @@ cudaError_t launch_resolve_slots(const int *slots, int batch, int nslots, int *r
     return cudaGetLastError();
 }
 
-// Segments of at least 128 tokens, as many as it takes to give every SM 16
-// warps of work.
+// Segments of at least 128 tokens, as many as it takes to give every SM 16 warps of
+// work (8: 71 against 63 us at 4 x 777 tokens, 8 heads of 128, N = 64; 32: the same).
 void causal_simt_segments(int batch, int L, int H, int P, int N, int sms, int *count, int *tokens) {
     const long long ctas = (long long)batch * H * (P / kCols);
     const long long want = 16LL * sms / (kCols * N / 1024);
