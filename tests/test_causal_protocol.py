@@ -11,8 +11,8 @@ then G.
 
 Each schedule (random heavy-tailed delays on loads and MMAs, random stepping) is
 checked for phase overruns, deadlock and stale reads. Planted variants that the
-model must catch: C released with G although C H reads it later, x released by the
-output although group C may still read it, diag(w) X written without waiting
+model must catch: C released with G although C H reads it later, x released by
+group C although Y and the output read it later, diag(w) X written without waiting
 for the MMAs of the half before, the state's copy written without waiting for C H
 of the tile before, and M written before G is complete.
 """
@@ -155,7 +155,8 @@ def group_c(S):
             yield ('write', 'h', n)
             yield ('arrive', 'H')
         yield ('arrive', ('VF', n % VEC))
-        if S.state or not S.planted.get('x_by_output'):
+        yield ('arrive', ('XE', n % 3))
+        if S.planted.get('x_by_c'):
             yield ('arrive', ('XE', n % 3))
 
 
@@ -174,8 +175,7 @@ def group(S, w):
         yield ('read', ('info', n % VEC), n)
         yield ('arrive', ('VF', n % VEC))
         yield ('arrive', ('GF', n % 2))
-        yield ('arrive', ('XE', n % 3))
-        if S.planted.get('x_by_output'):
+        if not S.planted.get('x_by_c'):
             yield ('arrive', ('XE', n % 3))
 
 
@@ -212,8 +212,8 @@ def test_model_catches_c_released_before_c_h_has_read_it():
     assert schedules(300, c_with_g=True)
 
 
-def test_model_catches_x_released_by_the_output_alone():
-    assert schedules(300, x_by_output=True)
+def test_model_catches_x_released_by_group_c_alone():
+    assert schedules(300, x_by_c=True)
 
 
 def test_model_catches_terms_written_under_the_mma():
