@@ -18,7 +18,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (SSD_PATH_AUTO, Workspace, ssd_block_step, ssd_prefix_state, ssd_prefix_state_layers)
+from . import (SSD_PATH_AUTO, Workspace, ssd_block_step, ssd_cache_compact, ssd_cache_copy, ssd_prefix_state,
+               ssd_prefix_state_layers)
 
 
 class BlockDiffusionCache:
@@ -47,6 +48,18 @@ class BlockDiffusionCache:
         ssd_prefix_state_layers(x, dt, A, B, init=self.state, out=self.state, chunk=chunk,
                                 workspace=self.ws_prefill)
         return self.state
+
+    def copy(self, src, dst):
+        """Row dst[i] of every layer's states becomes row src[i], or zero where
+        src[i] is -1 (int32, in this order): a prefix forked for several
+        continuations, a row freed for a new sequence (ssd_cache_copy)."""
+        return ssd_cache_copy(self.state, src, dst)
+
+    def compact(self, table):
+        """The rows that table (int32, -1 for none) names move to the front of
+        every layer's states (ssd_cache_compact): returns the table that goes with
+        them and their number."""
+        return ssd_cache_compact(self.state, table)
 
 
 class BlockGraph:

@@ -268,14 +268,12 @@ def ssd_cache_compact(pool, table, *, workspace: Workspace | None = None):
         raise ValueError("table is required")
     rows = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() == 1 else 0
     ptable = _whole(table, "table", _I32, dev, (rows,))
-    # the new table and the count, which share an allocation
-    both = table.new_empty((rows + 1,))
-    pnew = both.data_ptr()
+    new, live = torch.empty_like(table), table.new_empty((1,))
     stream = _raw_stream(dev.index)
     ws = _scratch(dev, stream, workspace)
     with ws.lock:
         buf = ws.get(256)
-        rc = lib.ssd_cache_compact(pool.data_ptr(), page, layers, nslots, ptable, rows, pnew, pnew + 4 * rows,
-                                   buf.data_ptr(), buf.numel(), stream)
+        rc = lib.ssd_cache_compact(pool.data_ptr(), page, layers, nslots, ptable, rows, new.data_ptr(),
+                                   live.data_ptr(), buf.data_ptr(), buf.numel(), stream)
     _check(rc, "ssd_cache_compact")
-    return both[:rows], both[rows:]
+    return new, live

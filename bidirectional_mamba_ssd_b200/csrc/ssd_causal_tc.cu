@@ -517,11 +517,10 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     ++mS;
                     moved = true;
                 } else if (!STATE) {
-                    // Y(n) = M X + C (half H); where the sequence ends in the tile, once group C has
-                    // zeroed what is behind it in x; past the one-factor mask C H goes to Yo, once
-                    // that of the tile before is read
+                    // Y(n) = M X + C (half H); the copy of H follows both halves of diag(w) X, so what
+                    // is behind the sequence's end in x is zero by now; past the one-factor mask C H
+                    // goes to Yo, once that of the tile before is read
                     if (nY < nG && mbar_test(bar(B_M_READY + (nY & 1)), (nY >> 1) & 1) && mbar_test(bar(B_H_READY), nY & 1) &&
-                        (2 * nY + 1 < mS || !(sm.info[nY % kVec].flags & kPartial)) &&
                         (nY == 0 || (sm.info[nY % kVec].flags & kOneFactor) ||
                          mbar_test(bar(B_G_FREE + ((nY - 1) & 1)), ((nY - 1) >> 1) & 1))) {
                         tc_fence_after();

@@ -420,3 +420,23 @@ def test_serving_run(ssd):
         for r, name in enumerate([0, None, 2, 3, 4]):
             if name is not None:
                 check_state(pool[l, table[r]], state[l, name], f"layer {l} row {r}")
+
+
+def test_block_diffusion_cache_rows(ssd):
+    """BlockDiffusionCache.copy and .compact on the cache that prefill fills."""
+    from bidirectional_mamba_ssd_b200.blockdiff import BlockDiffusionCache
+    layers, batch, H, N, L = 2, 6, 2, 64, 40
+    cache = BlockDiffusionCache(layers, batch, H, 64, N, device="cuda")
+    per = [inputs((batch, L), H, 64, N, 1, "bf16", seed=l) for l in range(layers)]
+    st = lambda k: torch.stack([p[k] for p in per]).contiguous()  # noqa: E731
+    before = cache.prefill(st("x"), st("dt"), st("A"), st("B")).clone()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache.copy(i32(5, -1), i32(1, 2))
+    want = before.clone()
+    want[:, 1], want[:, 2] = before[:, 5], 0
+    torch.cuda.synchronize()
+    assert torch.equal(cache.state, want)
+    table, live = cache.compact(i32(5, 1, -1, 3))
+    torch.cuda.synchronize()
+    assert live.item() == 3 and table.tolist() == [2, 1, -1, 0]
+    assert torch.equal(cache.state[:, 0], want[:, 3]) and torch.equal(cache.state[:, 2], want[:, 5])
