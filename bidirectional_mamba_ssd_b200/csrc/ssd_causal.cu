@@ -297,13 +297,15 @@ cudaError_t launch_resolve_slots(const int *slots, int batch, int nslots, int *r
     return cudaGetLastError();
 }
 
-// Segments of at least 128 tokens, as many as it takes to give every SM 16 warps of
-// work (8: 71 against 63 us at 4 x 777 tokens, 8 heads of 128, N = 64; 32: the same).
+// Segments of at least 64 tokens, as many as it takes to give every SM 16 warps of
+// work (4 x 777 tokens, 8 heads of 128, N = 64: 56 us; with 24 warps 65, 8 warps 71,
+// segments of at least 128 tokens 63; the second and third kernel launched ahead of
+// the one before's end 69).
 void causal_simt_segments(int batch, int L, int H, int P, int N, int sms, int *count, int *tokens) {
     const long long ctas = (long long)batch * H * (P / kCols);
     const long long want = 16LL * sms / (kCols * N / 1024);
     long long n = ctas > 0 ? want / ctas : 1;
-    const long long most = L / 128;
+    const long long most = L / 64;
     n = n < most ? n : most;
     if (n < 2) {
         *count = 1;
