@@ -346,6 +346,7 @@ cache_compact_kernel(const CacheArgs a) {
     const int live = sum_live;
     // set bits ahead of page s
     auto rank = [&](int s) { return before[s >> 5] + __popc(map[s >> 5] & ((1u << (s & 31)) - 1u)); };
+    // nothing to move in a pool of no layers or of empty pages: its table alone counts
     if (tid == 0) sum_moves = live == 0 || live >= a.nslots ? 0 : live - rank(live);
     __syncthreads();
     const int moves = sum_moves, stay = live - moves;
@@ -361,7 +362,7 @@ cache_compact_kernel(const CacheArgs a) {
     if constexpr (sizeof(V) == 16) {
         BulkSmem &sm = *reinterpret_cast<BulkSmem *>(shared);
         bulk_init(sm);
-        if (tid % 32 == 0 && tid < 32 * kMovers)
+        if (tid % 32 == 0 && tid < 32 * kMovers && a.layers > 0 && a.page_bytes > 0)
             bulk_move(
                 sm, a, tid / 32, moves, 951,
                 [&](int i, int &dst) {

@@ -132,3 +132,35 @@ def test_in_a_graph(ssd):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(data.cpu(), want) and new.tolist() == t and live.item() == n
+
+
+def test_long_lists_and_empty_pools(ssd):
+    """More pairs than are kept in shared memory, forks across that border; pools without layers or bytes."""
+    nslots = 4000
+    data = pool_of(2, nslots, (8,), seed=9)
+    p = list(range(nslots))
+    random.Random(4).shuffle(p)
+    src = [s for s in p[:500] for _ in range(3)] + [-1] * 300
+    dst = p[500:2000] + p[2000:2300]
+    src[1023:1027] = [p[400]] * 4
+    want = ref.copy(data, i32(src), i32(dst))
+    ssd.ssd_cache_copy(data, i32(src), i32(dst))
+    torch.cuda.synchronize()
+    assert torch.equal(data.cpu(), want)
+    # the same list over and over its own pages, in order
+    src, dst = (src * 2)[:2500], (dst + p[:1000])[:2500]
+    want = ref.copy(data, i32(src), i32(dst))
+    ssd.ssd_cache_copy(data, i32(src), i32(dst))
+    torch.cuda.synchronize()
+    assert torch.equal(data.cpu(), want)
+    for shape in ((0, 9, 8), (2, 9, 0), (2, 0, 8)):
+        empty = torch.zeros(shape, device="cuda")
+        t, live = ssd.ssd_cache_compact(empty, i32([7, 8, 2, -1]))
+        ssd.ssd_cache_copy(empty, i32([1]), i32([2]))
+        torch.cuda.synchronize()
+        if shape[1]:
+            assert t.tolist() == [0, 1, 2, -1] and live.item() == 3
+            assert ssd.ssd_get_device_status() == 0
+        else:
+            assert t.tolist() == [-1] * 4 and live.item() == 0
+            assert ssd.ssd_get_device_status() == ssd.SSD_ERR_INDEX

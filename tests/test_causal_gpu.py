@@ -86,6 +86,9 @@ SHAPES = [
     (1, 777, 6, 64, 128, 2, "bf16", True, True, False, False),
     (5, 300, 4, 64, 64, 4, "bf16", False, True, True, False),
     (1, 3000, 2, 64, 128, 1, "bf16", True, True, False, True),
+    (2, 200, 1, 256, 64, 1, "bf16", True, True, True, True),
+    (160, 20, 1, 64, 64, 1, "bf16", True, True, False, False),
+    (30, 300, 6, 64, 128, 1, "bf16", True, True, False, True),
     (1, 1, 4, 64, 128, 4, "f32", True, True, False, False),
     (3, 17, 4, 64, 128, 2, "f32", True, False, True, True),
     (2, 129, 2, 128, 64, 1, "f32", True, True, True, True),
@@ -440,3 +443,75 @@ def test_block_diffusion_cache_rows(ssd):
     torch.cuda.synchronize()
     assert live.item() == 3 and table.tolist() == [2, 1, -1, 0]
     assert torch.equal(cache.state[:, 0], want[:, 3]) and torch.equal(cache.state[:, 2], want[:, 5])
+
+
+def test_offsets_past_32_bits(ssd):
+    """x and out of more than 2^31 elements, and pages of a pool more than 2^32 bytes apart: the last row against a
+    call of its own, the last page against the recurrence."""
+    batch, L, H, P, N = 2, 16500, 512, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(batch, L, H, P, generator=g, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 2 ** 31
+    d = inputs((batch, L), H, 64, N, 1, "bf16", seed=4)
+    y, h = ssd.ssd_causal_fwd(x, d["dt"], d["A"], d["B"], d["C"], d["D"])
+    y1, h1 = ssd.ssd_causal_fwd(x[1:], d["dt"][1:], d["A"], d["B"][1:], d["C"][1:], d["D"])
+    torch.cuda.synchronize()
+    assert ssd.ssd_get_device_status() == 0
+    assert torch.equal(y[1:], y1) and torch.equal(h[1:], h1)
+    del x, y, y1, d
+    nslots, H, P, N = 6000, 24, 64, 128
+    pool = torch.zeros(nslots, H, P, N, device="cuda")
+    assert pool.numel() * 4 > 2 ** 32
+    d = inputs((2,), H, P, N, 1, "bf16", seed=5)
+    h0 = torch.randn(2, H, P, N, generator=g, device="cuda")
+    slots = torch.tensor([nslots - 1, nslots - 2], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = h0
+    one = lambda t: t[:, None]  # noqa: E731
+    o, oh = ref.fwd(one(d["x"]), one(sizes(d)), d["A"], one(d["B"]), one(d["C"]), d["D"], h0, [1, 1])
+    y = ssd.ssd_causal_step(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], pool, slots)
+    ssd.ssd_cache_copy(pool[None], slots, torch.tensor([1, nslots - 3], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    check_out(y, o[:, 0], "bf16", "last pages")
+    check_state(pool[slots.long()], oh, "last pages")
+    assert torch.equal(pool[1], pool[nslots - 1]) and torch.equal(pool[nslots - 3], pool[nslots - 2])
+    t, live = ssd.ssd_cache_compact(pool[None], slots)
+    assert live.item() == 2 and t.tolist() == [1, 0]
+    check_state(pool[:2], oh.flip(0), "moved pages")
+
+
+def test_out_aligned_to_16_bytes_only(ssd):
+    """An output 16 bytes off a 32-byte boundary."""
+    d = inputs((2, 200), 2, 64, 64, 1, "bf16", seed=6)
+    a = [d[k] for k in ("x", "dt", "A", "B", "C", "D")]
+    y, h = ssd.ssd_causal_fwd(*a)
+    room = torch.zeros(d["x"].numel() + 16, dtype=torch.bfloat16, device="cuda")
+    out = room[8:8 + d["x"].numel()].view(d["x"].shape)
+    assert out.data_ptr() % 32 == 16
+    y2, h2 = ssd.ssd_causal_fwd(*a, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(h, h2) and (room[:8] == 0).all() and (room[8 + y.numel():] == 0).all()
+
+
+def test_many_rows_and_all_skipped(ssd):
+    """More rows than threads of a block, lengths all over; a batch of padding rows only."""
+    batch, L, H, N = 700, 70, 1, 64
+    d = inputs((batch, L), H, 64, N, 1, "bf16", seed=13)
+    lens = [int(v) for v in torch.randint(0, L + 1, (batch,), generator=torch.Generator().manual_seed(1))]
+    lens[300:500] = [0] * 200
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, oh = ref.fwd(d["x"], sizes(d), d["A"], d["B"], d["C"], d["D"], torch.zeros(batch, H, 64, N), lens)
+    y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], seqlens=seqlens)
+    torch.cuda.synchronize()
+    check_out(y, o, "bf16", "many rows")
+    check_state(h, oh, "many rows")
+    # values outside [0, L] are clamped
+    y2, h2 = ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"],
+                                seqlens=torch.where(seqlens == L, 1 << 30, torch.where(seqlens == 0, -5, seqlens)).to(torch.int32))
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    pool = torch.ones(3, H, 64, N, device="cuda")
+    none = torch.full((batch,), -1, dtype=torch.int32, device="cuda")
+    for path in paths_of(ssd, "bf16"):
+        y3, _ = ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], pool, slots=none, path=path)
+        torch.cuda.synchronize()
+        assert (y3 == 0).all() and (pool == 1).all()
+    assert ssd.ssd_get_device_status() == 0
