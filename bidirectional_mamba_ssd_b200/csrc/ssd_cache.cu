@@ -12,9 +12,10 @@
 // same element of the page in every pair; where pairs do not stand apart one
 // thread applies the whole list to its element in order, which is the order's
 // meaning and needs no synchronisation.
-// Measured on 16 pages to two others each and 8 cleared, 24 layers of 786 KB (1.06
-// GB): see the table of the kernel's figures; a copy through registers (8 loads of
-// 16 bytes a thread in flight) took 238 us.
+// Measured on 24 layers with pages of 786 KB: 16 pages to two others each and 8
+// cleared (1.06 GB) 189 us, 5.6 TB/s, where a copy through registers (8 loads of 16 bytes
+// a thread in flight) took 238 us; compaction of 12 layers with 30 moves (566 MB) 97.8 us,
+// 5.8 TB/s (registers: 153 us).
 #include <stdint.h>
 
 #include "sm100.cuh"

@@ -24,7 +24,15 @@
 // state is a result in fp32, so diag(w) X enters S as three bf16 terms (24 bits),
 // and H stays in fp32 registers.
 //
-// What bounds it: HBM (x, B, C and y once). Work is cut so that every CTA has
+// What bounds it: on paper HBM (x, B, C and y once); as measured the work of a tile
+// within an SM. 32 x 1024 tokens, 24 heads of 64, N = 128 (631 MB, 96 us at the rate of
+// a copy): 132 us in a short run at 1.96 GHz, 153 to 163 us in a long one, where the
+// power limit holds the clock near 1.55 GHz. A tile takes an SM about 4700 cycles:
+// nearly 3000 of shared-memory traffic (the MMAs' operands and the terms of diag(w) X),
+// around which mask, state and output have to fit. One sequence of 65536 tokens (1.21
+// GB, 185 us): 418 us, of which the pass for the states 134 and the outputs 250.
+//
+// Work is cut so that every CTA has
 // the same number of tiles: the tiles of all units in order, divided evenly. A
 // unit that a cut falls into is shared by two neighbouring CTAs. With a unit or
 // more per CTA the first part of a shared unit is its CTA's first work and the
@@ -1162,9 +1170,12 @@ cudaError_t run_tc(const CausalArgs &a, void *scratch, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const long long units = (long long)a.batch * p.HU, nt = (a.L + kTile - 1) / kTile;
     // fewer units than SMs: the cut work costs a second pass over x and B and two
-    // more launches, but spreads over every SM
+    // more launches, but spreads over every SM. Whole units take about 2.4 us a tile, cut
+    // ones 4 us a tile of the largest share and 10 us. Whole and cut, 24 units: 768 tokens
+    // 19.7 and 19.7 us, 1024 24.5 and 23.1, 4096 83 and 39; 48 units: 1024 24.9 and 27.5,
+    // 1536 34.7 and 31.8; 96 units: 4096 84 and 100
     const long long share = (units * nt + sms - 1) / sms;
-    p.order = units >= sms ? kOrderHandoff : 10 * nt > 16 * share + 60 ? kOrderNatural : kOrderWhole;
+    p.order = units >= sms ? kOrderHandoff : 10 * nt > 16 * share + 40 ? kOrderNatural : kOrderWhole;
     const bool ragged = a.seqlens || a.slots, first = ragged || p.order == kOrderHandoff;
     if (first) {
         int *rows = reinterpret_cast<int *>(ws + t.rows), *lens = reinterpret_cast<int *>(ws + t.lens);
