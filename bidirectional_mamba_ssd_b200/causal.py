@@ -24,6 +24,7 @@ import torch
 from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _DT, _workspace, lib)
 
 _INF = float("inf")
+_INT = 2**31 - 1
 _F32, _I32 = torch.float32, torch.int32
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -231,6 +232,8 @@ def _pages(pool):
     if len(shape) < 3 or not pool.is_contiguous():
         raise ValueError(f"pool must be (layers, slots, page...), contiguous (got {tuple(shape)}, strides {pool.stride()})")
     layers, nslots = shape[0], shape[1]
+    if layers > _INT or nslots > _INT:
+        raise ValueError(f"pool: more than {_INT} layers or slots (got {tuple(shape)})")
     return dev, layers, nslots, pool.element_size() * shape[2:].numel()
 
 
@@ -246,6 +249,8 @@ def ssd_cache_copy(pool, src, dst, *, workspace: Workspace | None = None):
         raise ValueError("src and dst are required")
     n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
     ps, pd = _whole(src, "src", _I32, dev, (n,)), _whole(dst, "dst", _I32, dev, (n,))
+    if n > _INT:
+        raise ValueError(f"src and dst have more than {_INT} entries")
     stream = _raw_stream(dev.index)
     ws = _scratch(dev, stream, workspace)
     with ws.lock:
@@ -268,6 +273,8 @@ def ssd_cache_compact(pool, table, *, workspace: Workspace | None = None):
         raise ValueError("table is required")
     rows = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() == 1 else 0
     ptable = _whole(table, "table", _I32, dev, (rows,))
+    if rows > _INT:
+        raise ValueError(f"table has more than {_INT} entries")
     new, live = torch.empty_like(table), table.new_empty((1,))
     stream = _raw_stream(dev.index)
     ws = _scratch(dev, stream, workspace)

@@ -412,6 +412,7 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
  *  - dt_bias NULL: dt is the step size. Otherwise it is the raw projection and
  *    the step size min(max(softplus(dt + dt_bias[h]), dt_min), dt_max), as for
  *    ssd_bidir_fwd_dtraw, kept in fp32. D may be NULL (no skip term).
+ *  - A <= 0 and step sizes >= 0, as above; device memory is not checked for it.
  *  - Forward only: there is no backward pass of these calls. */
 
 /* Prompts: from the start state (page of init_state, or zero where it is NULL),
@@ -429,7 +430,7 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
  *   out      (batch, seqlen, nheads, headdim)      io, contiguous, overwritten
  *   state_out pool fp32, nullable (the end states are not wanted)
  * Within a sequence a non-finite input makes the outputs of its own tile of 128
- * tokens undefined, not only those behind it.
+ * tokens undefined, not only those behind it, and the end state.
  * path: SSD_PATH_AUTO, SSD_PATH_SIMT (the CUDA-core scan, either dtype) or
  * SSD_PATH_FUSED (the tensor-core kernel, bf16; what AUTO takes for bf16). With
  * bf16 the state is carried and returned in fp32 with fp32 accuracy on either

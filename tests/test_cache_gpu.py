@@ -164,3 +164,14 @@ def test_long_lists_and_empty_pools(ssd):
         else:
             assert t.tolist() == [-1] * 4 and live.item() == 0
             assert ssd.ssd_get_device_status() == ssd.SSD_ERR_INDEX
+
+
+def test_sizes_past_32_bits_are_refused(ssd):
+    """Layers and slots are 32-bit at the boundary: more of them raise instead of wrapping."""
+    idx = i32([0])
+    for shape in ((2**31, 1, 0), (1, 2**32 + 4, 0)):
+        pool = torch.empty(shape, dtype=torch.uint8, device="cuda")
+        with pytest.raises(ValueError):
+            ssd.ssd_cache_copy(pool, idx, idx)
+        with pytest.raises(ValueError):
+            ssd.ssd_cache_compact(pool, idx)
