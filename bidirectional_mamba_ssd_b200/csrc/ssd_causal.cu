@@ -6,13 +6,19 @@
 //
 // The state's columns p do not depend on one another, so a CTA takes COLS of a
 // head's P columns and walks its tokens with that part of the state in
-// registers: a thread owns 4 p x 8 n, reads 20 operands a token from shared memory
-// for its 96 operations (packed two to an instruction, f32x2) and meets the other n in
-// a butterfly. Tokens arrive in chunks of kTok through cp.async, two chunks deep. What
-// bounds it: instruction issue with many units (64 x 500 tokens, 24 heads of 64, N =
-// 128: 581 us, where 2 p a thread take 706 us and 16 columns a CTA about as long), a
-// warp's own time per token with few; there the sequence is cut into segments (own
-// end states, a carry, then the outputs), which costs a second pass over x and B.
+// registers: a thread owns 4 p x 8 n, reads 20 operands a token from shared memory and
+// meets the other n in a butterfly; its arithmetic is packed two to an instruction
+// (f32x2). Four tokens share one rescaling of the state: with d_s the decay behind token
+// s among the four,
+//   H <- exp(all) H ahead of the first, H <- H + exp(d_s) dt_s x_s B_s^T, y_t = exp(-d_t) H C_t
+// leaves the state itself behind the fourth (d = 0). Where the four decay by more than
+// e^-4 each token rescales as it is written above. Tokens arrive in chunks of kTok through
+// cp.async, two chunks deep.
+// What bounds it: with many units instruction issue and shared memory together (64 x
+// 500 tokens, 24 heads of 64, N = 128: 541 us; 581 us with a rescaling every token; 8 p a
+// thread 566 us, 2 p 706 against 581), with few a warp's own time per token; there the
+// sequence is cut into segments (own end states, a carry, then the outputs), which costs
+// a second pass over x and B.
 #include <stdint.h>
 
 #include "ssd_causal.h"
@@ -64,8 +70,12 @@ __device__ __forceinline__ float4 lds4(const __nv_bfloat16 *p) {
 template <typename T, int N, int COLS>
 struct SimtSmem {
     T B[2][kTok][N], C[2][kTok][N], x[2][kTok][COLS];
-    float2 gd[2][kTok];   // decay and step size of a token
+    float4 f[2][kTok];    // a token's factors: of the state ahead of it, of x B^T, of the output; whether the first is due
 };
+
+// Decay of four tokens up to which they share one rescaling of the state (past it
+// exp(d) would magnify the rounding of d).
+constexpr float kMaxQuad = 4.f;
 
 template <typename T, int N, int COLS, int MODE>
 __global__ void __launch_bounds__(COLS *N / (8 * KP))
@@ -143,9 +153,17 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     if (first < end) fetch(first, 0);
     for (int t0 = first; t0 < end; t0 += kTok, buf ^= 1) {
         const int m = min(kTok, end - t0);
-        if (tid < m) {
-            const float v = a.step(raw_dt, h);
-            sm.gd[buf][tid] = make_float2(expf(v * A), v);
+        if (warp == 0) {
+            const float v = tid < m ? a.step(raw_dt, h) : 0.f;
+            const float v1 = __shfl_down_sync(0xffffffffu, v, 1), v2 = __shfl_down_sync(0xffffffffu, v, 2),
+                        v3 = __shfl_down_sync(0xffffffffu, v, 3);
+            const int q = lane & 3;
+            const float after = (q < 3 ? v1 : 0.f) + (q < 2 ? v2 : 0.f) + (q < 1 ? v3 : 0.f);
+            const float all = A * __shfl_sync(0xffffffffu, v + after, lane & ~3), d = A * after;
+            const bool quad = fabsf(all) <= kMaxQuad;
+            if (tid < m)
+                sm.f[buf][tid] = quad ? make_float4(expf(all), expf(d) * v, expf(-d), q == 0 ? 1.f : 0.f)
+                                      : make_float4(expf(v * A), v, 1.f, 1.f);
             sum += v;
         }
         cp_wait();
@@ -153,18 +171,24 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
         if (t0 + kTok < end) fetch(t0 + kTok, buf ^ 1);
 #pragma unroll 4
         for (int t = 0; t < m; ++t) {
-            const float2 gd = sm.gd[buf][t];
+            const float4 f = sm.f[buf][t];
             const float4 x = lds4(&sm.x[buf][t][KP * cg]);
             float xs[KP] = {x.x, x.y, x.z, x.w};
             const float4 b0 = lds4(&sm.B[buf][t][4 * gn]), b1 = lds4(&sm.B[buf][t][N / 2 + 4 * gn]);
             const f32x2 Bv[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
-            const f32x2 G = pack2(gd.x, gd.x);
+            if (f.w != 0.f) {
+                const f32x2 G = pack2(f.x, f.x);
+#pragma unroll
+                for (int k = 0; k < KP; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) H[k][q] = mul2(H[k][q], G);
+            }
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
-                const float u = gd.y * xs[k];
+                const float u = f.y * xs[k];
                 const f32x2 U = pack2(u, u);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) H[k][q] = fma2(H[k][q], G, mul2(U, Bv[q]));
+                for (int q = 0; q < 4; ++q) H[k][q] = fma2(U, Bv[q], H[k][q]);
             }
             if (OUT) {
                 const float4 c0 = lds4(&sm.C[buf][t][4 * gn]), c1 = lds4(&sm.C[buf][t][N / 2 + 4 * gn]);
@@ -193,7 +217,7 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
 #pragma unroll
                 for (; o >= 1; o >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
                 if ((gn & (NG / KP - 1)) == 0)
-                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + KP * cg + keep, a.D ? fmaf(D, xs[0], y[0]) : y[0]);
+                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + KP * cg + keep, a.D ? fmaf(D, xs[0], f.z * y[0]) : f.z * y[0]);
             }
         }
     }

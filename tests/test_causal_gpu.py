@@ -515,3 +515,20 @@ def test_many_rows_and_all_skipped(ssd):
         torch.cuda.synchronize()
         assert (y3 == 0).all() and (pool == 1).all()
     assert ssd.ssd_get_device_status() == 0
+
+
+def test_fp32_scan_decay_of_four_tokens(ssd):
+    """The CUDA-core scan rescales the state once for four tokens whose decay is at most e^-4: step sizes of 0.1 with
+    decays of e^-3.9, e^-4.1 a four, and heads that change within the sequence, at lengths that end inside a four."""
+    A = torch.tensor([-9.75, -10.25, -1.0], device="cuda")
+    for L in (1, 3, 6, 33, 203):
+        d = inputs((1, L), 3, 64, 64, 1, "f32", seed=20 + L)
+        d["dt"][:, :, :2] = 0.1
+        d["dt"][:, ::7, 2] = 30.0
+        h0 = torch.randn(1, 3, 64, 64, generator=d["g"], device="cuda")
+        o, oh = ref.fwd(d["x"], sizes(d), A, d["B"], d["C"], d["D"], h0, [L])
+        y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], A, d["B"], d["C"], d["D"], h0)
+        torch.cuda.synchronize()
+        for k in range(3):
+            check_out(y[:, :, k], o[:, :, k], "f32", f"L {L} head {k}")
+            check_state(h[:, k], oh[:, k], f"L {L} head {k}")
