@@ -1,15 +1,19 @@
-"""Build libssd_bidir.so in-tree with nvcc for sm_100a.
+"""Build libssd_bidir.so in-tree with nvcc for sm_100a, and the Python binding's
+C++ part.
 
 Each .cu under csrc/ is compiled to an object in _build/ and the objects are
 linked into bidirectional_mamba_ssd_b200/libssd_bidir.so. Sources are rebuilt
-when they (or a header) are newer than their object.
+when they (or a header) are newer than their object. csrc/ssd_binding.cpp
+(torch's C++ headers, no CUDA code) becomes _binding.so beside it.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd_bidir.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -53,7 +58,27 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "ssd_binding.cpp")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()):
+        return BINDING
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE]
+    for d in (sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+              os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda):
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

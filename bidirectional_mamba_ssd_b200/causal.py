@@ -12,16 +12,25 @@ their last two dimensions (dt: its last) are contiguous.
 Calls without a workspace of their own use the stream's, or, while a CUDA graph
 is being captured, one that belongs to the graph: two graphs never share one.
 
-A single token's kernel takes a few microseconds, so the checks here are written
-to cost little: one pass over each tensor, no objects made on the way.
+A single token's kernel takes a few microseconds, less than ctypes takes to call it. So
+each function first offers its arguments to csrc/ssd_binding.cpp, which makes the
+call if all of them are as they should be; what follows here is for the calls that it
+leaves alone: bad arguments (their messages), another device than the current one,
+a workspace that has yet to be made or to grow, and a graph's own under capture.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import torch
 
-from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _DT, _workspace, lib)
+from . import _binding
+from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _default_ws, _DT, _workspace,
+               lib)
+
+_binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                 (lib.ssd_causal_fwd, lib.ssd_causal_step, lib.ssd_cache_copy, lib.ssd_cache_compact)), _default_ws, _check)
 
 _INF = float("inf")
 _INT = 2**31 - 1
@@ -122,6 +131,10 @@ def ssd_causal_fwd(x, dt, A, B, C, D=None, init=None, *, seqlens=None, slots=Non
     (nslots, H, P, N) whose page slots[b] is row b's; None starts from zero.
     state_out: where the end states go, laid out as init; with slots it
     defaults to init (in place). dt_bias (H): dt is the raw projection."""
+    got = _binding.causal_fwd(x, dt, A, B, C, D, init, seqlens, slots, dt_bias, dt_min, dt_max, out, state_out, path,
+                              workspace)
+    if got is not NotImplemented:
+        return got
     dev, io, xshape = _lead(x, "x", 4)
     if dev.index != _device():
         with torch.cuda.device(dev):
@@ -176,6 +189,9 @@ def ssd_causal_step(x, dt, A, B, C, D, states, slots=None, *, dt_bias=None, dt_m
     P), dt (batch, H), B, C (batch, G, N), D (H) or None. The states, (batch, H,
     P, N) or with slots (batch) int32 a pool of pages, advance in place unless
     state_out is given. Returns out like x."""
+    got = _binding.causal_step(x, dt, A, B, C, D, states, slots, dt_bias, dt_min, dt_max, out, state_out, workspace)
+    if got is not NotImplemented:
+        return got
     dev, io, xshape = _lead(x, "x", 3)
     if dev.index != _device():
         with torch.cuda.device(dev):
@@ -241,6 +257,9 @@ def ssd_cache_copy(pool, src, dst, *, workspace: Workspace | None = None):
     """Pages of a pool (layers, slots, ...) of any dtype, in place and in every
     layer: page dst[i] <- page src[i], or zero where src[i] is -1, in the order
     of i (include/ssd_bidir.h: ssd_cache_copy). src, dst (n) int32. Returns pool."""
+    got = _binding.cache_copy(pool, src, dst, workspace)
+    if got is not NotImplemented:
+        return got
     dev, layers, nslots, page = _pages(pool)
     if dev.index != _device():
         with torch.cuda.device(dev):
@@ -265,6 +284,9 @@ def ssd_cache_compact(pool, table, *, workspace: Workspace | None = None):
     pool (layers, slots, ...), in place, with the fewest moves (include/
     ssd_bidir.h: ssd_cache_compact). Returns (the table that goes with the moved
     pages, the number of live pages as an int32 tensor of one)."""
+    got = _binding.cache_compact(pool, table, workspace)
+    if got is not NotImplemented:
+        return got
     dev, layers, nslots, page = _pages(pool)
     if dev.index != _device():
         with torch.cuda.device(dev):

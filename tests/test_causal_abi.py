@@ -85,3 +85,17 @@ def test_step_and_cache_entry_points_reject_bad_arguments(lib):
     assert compact(rows=-1) == -1 and compact(nslots=(1 << 18) + 1) == -2 and compact(ws=0) == -4
     assert compact(pool=0) == -1 and compact(table=0) == -1 and compact(out=0) == -1 and compact(live=0) == -1
     assert compact(out=FAKE) == -1 and compact(out=FAKE + 8) == -1       # the tables overlap
+
+
+def test_binding_leaves_what_is_not_its_own():
+    """The C++ part of the binding makes no call of CPU tensors or of things that are none, and raises nothing for them."""
+    import torch
+    from bidirectional_mamba_ssd_b200 import _binding
+    x = torch.zeros(2, 3, 4)
+    for a in (x, None, 1, "x", torch.zeros(2, 3, 4, 5), torch.empty(3, 4, 5, device="meta")):
+        assert _binding.causal_fwd(*[a] * 16) is NotImplemented
+        assert _binding.causal_step(*[a] * 14) is NotImplemented
+        assert _binding.cache_copy(*[a] * 4) is NotImplemented
+        assert _binding.cache_compact(*[a] * 3) is NotImplemented
+    with pytest.raises(TypeError):
+        _binding.causal_step(x)

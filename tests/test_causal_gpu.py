@@ -532,3 +532,60 @@ def test_fp32_scan_decay_of_four_tokens(ssd):
         for k in range(3):
             check_out(y[:, :, k], o[:, :, k], "f32", f"L {L} head {k}")
             check_state(h[:, k], oh[:, k], f"L {L} head {k}")
+
+
+class _Declines:
+    """Stands for the binding's C++ part: leaves every call to the Python way."""
+    causal_fwd = causal_step = cache_copy = cache_compact = staticmethod(lambda *a: NotImplemented)
+
+
+@pytest.mark.parametrize("io,packed,raw", [("bf16", True, True), ("f32", False, False)])
+def test_both_ways_of_the_binding(ssd, monkeypatch, io, packed, raw):
+    """The C++ and the Python way of the same calls: the same outputs, states, pages and errors; each is taken."""
+    from bidirectional_mamba_ssd_b200 import _binding, causal
+    d = inputs((3, 70), 2, 64, 64, 1, io, packed=packed, raw=raw, seed=31)
+    t = inputs((3,), 2, 64, 64, 1, io, packed=packed, raw=raw, seed=32)
+    slots = torch.tensor([4, 1, 3], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([70, 0, 33], dtype=torch.int32, device="cuda")
+    src, dst = slots, torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    ws = ssd.Workspace(torch.device("cuda", 0))
+    ws.get(1 << 24)
+    names = ("causal_fwd", "causal_step", "cache_copy", "cache_compact")
+
+    def run():
+        pool = torch.ones(2, 6, 2, 64, 64, device="cuda")
+        given = torch.empty(3, 2, 64, dtype=t["x"].dtype, device="cuda")
+        got = list(ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], pool[0], slots=slots, seqlens=lens,
+                                      workspace=ws, **opts(d)))
+        got += list(ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], path=ssd.SSD_PATH_SIMT, workspace=ws, **opts(d)))
+        assert got[1].data_ptr() == pool[0].data_ptr()
+        ssd.ssd_cache_copy(pool, src, dst, workspace=ws)
+        got.append(ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], t["D"], pool[0], dst, workspace=ws, **opts(t)))
+        y = ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], None, pool[1, :3], out=given,
+                                state_out=pool[1, 3:], **opts(t))
+        assert y is given
+        got += [y, pool]
+        got += list(ssd.ssd_cache_compact(pool, slots, workspace=ws))
+        with pytest.raises(ssd.SSDError):
+            ssd.ssd_causal_step(t["x"][..., :32].contiguous(), t["dt"], t["A"], t["B"], t["C"], None, pool[0, :3, :, :32].contiguous())
+        with pytest.raises(ValueError):
+            ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], None, pool[0, :3], state_out=pool.view(-1)[64:].narrow(
+                0, 0, 3 * 2 * 64 * 64).view(3, 2, 64, 64))
+        torch.cuda.synchronize()
+        assert ws.status() == 0
+        return [g.clone() for g in got]
+
+    took = []
+    spy = type("Spy", (), {n: staticmethod(lambda *a, n=n: _took(took, n, getattr(_binding, n)(*a))) for n in names})
+    monkeypatch.setattr(causal, "_binding", spy)
+    first = run()
+    assert set(took) == set(names)
+    monkeypatch.setattr(causal, "_binding", _Declines)
+    for k, (a, b) in enumerate(zip(first, run())):
+        assert a.dtype == b.dtype and torch.equal(a, b), f"result {k}"
+
+
+def _took(took, name, got):
+    if got is not NotImplemented:
+        took.append(name)
+    return got
