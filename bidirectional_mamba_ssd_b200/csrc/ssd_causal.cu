@@ -52,9 +52,10 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     return d;
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+// 16 bytes, zeros where `there` is false (the address is not read)
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool there) {
     const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
@@ -67,15 +68,24 @@ __device__ __forceinline__ float4 lds4(const __nv_bfloat16 *p) {
                        __uint_as_float(v.y & 0xffff0000u));
 }
 
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_row(float *p, const float (&v)[1]) { p[0] = v[0]; }
+__device__ __forceinline__ void store_row(float *p, const float (&v)[2]) { *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]); }
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&v)[1]) { p[0] = __float2bfloat16_rn(v[0]); }
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&v)[2]) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
+}
+
 template <typename T, int N, int COLS>
 struct SimtSmem {
     T B[2][kTok][N], C[2][kTok][N], x[2][kTok][COLS];
-    float4 f[2][kTok];    // a token's factors: of the state ahead of it, of x B^T, of the output; whether the first is due
+    float4 f[2][kTok];    // a token's factors: of the state ahead of it, of x B^T, of the output; 1 if its four go one by one
 };
 
-// Decay of four tokens up to which they share one rescaling of the state (past it
-// exp(d) would magnify the rounding of d).
-constexpr float kMaxQuad = 4.f;
+// Decay of four tokens up to which they share one rescaling of the state: e^d carries
+// the rounding of d, 2^-24 of it, to the terms of the same four.
+constexpr float kMaxQuad = 8.f;
 
 template <typename T, int N, int COLS, int MODE>
 __global__ void __launch_bounds__(COLS *N / (8 * KP))
@@ -136,14 +146,17 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     auto fetch = [&](int t0, int buf) {
         const int m = min(kTok, end - t0);
         constexpr int EPC = 16 / (int)sizeof(T);
-        for (int i = tid; i < m * (N / EPC); i += THREADS) {
+#pragma unroll
+        for (int i = tid; i < kTok * (N / EPC); i += THREADS) {
             const int t = i / (N / EPC), c = (i % (N / EPC)) * EPC;
-            cp_async16(&sm.B[buf][t][c], Bp + (long long)(t0 + t) * a.b_st + c);
-            if (OUT) cp_async16(&sm.C[buf][t][c], Cp + (long long)(t0 + t) * a.c_st + c);
+            const long long at = t0 + (t < m ? t : 0);
+            cp_async16(&sm.B[buf][t][c], Bp + at * a.b_st + c, t < m);
+            if (OUT) cp_async16(&sm.C[buf][t][c], Cp + at * a.c_st + c, t < m);
         }
-        for (int i = tid; i < m * (COLS / EPC); i += THREADS) {
+#pragma unroll
+        for (int i = tid; i < kTok * (COLS / EPC); i += THREADS) {
             const int t = i / (COLS / EPC), c = (i % (COLS / EPC)) * EPC;
-            cp_async16(&sm.x[buf][t][c], xp + (long long)(t0 + t) * a.x_st + c);
+            cp_async16(&sm.x[buf][t][c], xp + (t0 + (t < m ? t : 0)) * a.x_st + c, t < m);
         }
         cp_commit();
         if (tid < m) raw_dt = IO<T>::load(dtp + (long long)(t0 + tid) * a.dt_st);
@@ -161,64 +174,78 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
             const float after = (q < 3 ? v1 : 0.f) + (q < 2 ? v2 : 0.f) + (q < 1 ? v3 : 0.f);
             const float all = A * __shfl_sync(0xffffffffu, v + after, lane & ~3), d = A * after;
             const bool quad = fabsf(all) <= kMaxQuad;
-            if (tid < m)
-                sm.f[buf][tid] = quad ? make_float4(expf(all), expf(d) * v, expf(-d), q == 0 ? 1.f : 0.f)
-                                      : make_float4(expf(v * A), v, 1.f, 1.f);
+            if (tid < kTok)
+                sm.f[buf][tid] = quad ? make_float4(expf(all), expf(d) * v, expf(-d), 0.f) : make_float4(expf(v * A), v, 1.f, 1.f);
             sum += v;
         }
         cp_wait();
         __syncthreads();      // chunk here; the other buffer is read by nobody
         if (t0 + kTok < end) fetch(t0 + kTok, buf ^ 1);
-#pragma unroll 4
-        for (int t = 0; t < m; ++t) {
-            const float4 f = sm.f[buf][t];
-            const float4 x = lds4(&sm.x[buf][t][KP * cg]);
-            float xs[KP] = {x.x, x.y, x.z, x.w};
-            const float4 b0 = lds4(&sm.B[buf][t][4 * gn]), b1 = lds4(&sm.B[buf][t][N / 2 + 4 * gn]);
-            const f32x2 Bv[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
-            if (f.w != 0.f) {
-                const f32x2 G = pack2(f.x, f.x);
+        // four tokens at a time (the last chunk's are filled up with zeros), or, where they
+        // go one by one, one of the four at a time
+#pragma unroll 1
+        for (int j = 0; j < m;) {
+            const bool single = sm.f[buf][j].w != 0.f;
+            const int t4 = j & ~3;
+            const f32x2 G = pack2(sm.f[buf][j].x, sm.f[buf][j].x);
 #pragma unroll
-                for (int k = 0; k < KP; ++k)
+            for (int k = 0; k < KP; ++k)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) H[k][q] = mul2(H[k][q], G);
-            }
+                for (int q = 0; q < 4; ++q) H[k][q] = mul2(H[k][q], G);
+            float y[4 * KP];      // of token i and column k: y[KP * i + k]
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const float u = f.y * xs[k];
-                const f32x2 U = pack2(u, u);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) H[k][q] = fma2(U, Bv[q], H[k][q]);
-            }
-            if (OUT) {
-                const float4 c0 = lds4(&sm.C[buf][t][4 * gn]), c1 = lds4(&sm.C[buf][t][N / 2 + 4 * gn]);
-                const f32x2 Cv[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
-                float y[KP];
+            for (int i = 0; i < 4; ++i) {
+                const int t = t4 + i;
+                const float fy = !single || t == j ? sm.f[buf][t].y : 0.f;
+                const float4 x = lds4(&sm.x[buf][t][KP * cg]);
+                const float xs[KP] = {x.x, x.y, x.z, x.w};
+                const float4 b0 = lds4(&sm.B[buf][t][4 * gn]), b1 = lds4(&sm.B[buf][t][N / 2 + 4 * gn]);
+                const f32x2 Bv[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
-                    const f32x2 s = fma2(H[k][3], Cv[3], fma2(H[k][2], Cv[2], fma2(H[k][1], Cv[1], mul2(H[k][0], Cv[0]))));
-                    const float2 f = unpack2(s);
-                    y[k] = f.x + f.y;
-                }
-                // butterfly over the NG lanes of a column group: the first steps halve the
-                // columns a lane carries, the others add
-                int keep = 0, o = NG / 2;
+                    const float u = fy * xs[k];
+                    const f32x2 U = pack2(u, u);
 #pragma unroll
-                for (int m = KP / 2; m >= 1; m >>= 1, o >>= 1) {
+                    for (int q = 0; q < 4; ++q) H[k][q] = fma2(U, Bv[q], H[k][q]);
+                }
+                if (OUT) {
+                    const float4 c0 = lds4(&sm.C[buf][t][4 * gn]), c1 = lds4(&sm.C[buf][t][N / 2 + 4 * gn]);
+                    const f32x2 Cv[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) {
+                        const f32x2 s = fma2(H[k][3], Cv[3], fma2(H[k][2], Cv[2], fma2(H[k][1], Cv[1], mul2(H[k][0], Cv[0]))));
+                        const float2 v = unpack2(s);
+                        y[KP * i + k] = v.x + v.y;
+                    }
+                }
+            }
+            if (OUT) {
+                // butterfly over the NG lanes of a column group: each step halves the values a
+                // lane carries, until it has one column (NG = 16) or two (8) of one token
+                constexpr int LEFT = 4 * KP / NG;
+#pragma unroll
+                for (int n = 2 * KP, o = NG / 2; o >= 1; n >>= 1, o >>= 1) {
                     const bool up = gn & o;
 #pragma unroll
-                    for (int k = 0; k < m; ++k) {
-                        const float send = up ? y[k] : y[k + m], mine = up ? y[k + m] : y[k];
+                    for (int k = 0; k < n; ++k) {
+                        const float send = up ? y[k] : y[k + n], mine = up ? y[k + n] : y[k];
                         y[k] = mine + __shfl_xor_sync(0xffffffffu, send, o);
-                        xs[k] = up ? xs[k + m] : xs[k];
                     }
-                    keep += up ? m : 0;
                 }
+                const int first_of = gn * LEFT, t = t4 + first_of / KP, k = KP * cg + first_of % KP;
+                if (t < m && (!single || t == j)) {
+                    const float fz = sm.f[buf][t].z;
+                    T *dst = out + (size_t)(t0 + t) * a.H * a.P + k;
+                    float v[LEFT];
 #pragma unroll
-                for (; o >= 1; o >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
-                if ((gn & (NG / KP - 1)) == 0)
-                    IO<T>::store(out + (size_t)(t0 + t) * a.H * a.P + KP * cg + keep, a.D ? fmaf(D, xs[0], f.z * y[0]) : f.z * y[0]);
+                    for (int q = 0; q < LEFT; ++q) {
+                        v[q] = fz * y[q];
+                        if (a.D) v[q] = fmaf(D, to_float(sm.x[buf][t][k + q]), v[q]);
+                    }
+                    store_row(dst, v);
+                }
             }
+            j = single ? j + 1 : t4 + 4;
         }
     }
     if (OUT) blank(end);
