@@ -6,19 +6,19 @@
 //
 // The state's columns p do not depend on one another, so a CTA takes COLS of a
 // head's P columns and walks its tokens with that part of the state in
-// registers: a thread owns 4 p x 8 n, reads 20 operands a token from shared memory and
-// meets the other n in a butterfly; its arithmetic is packed two to an instruction
-// (f32x2). Four tokens share one rescaling of the state: with d_s the decay behind token
-// s among the four,
+// registers: a thread owns 4 p x 8 n and works on four tokens at a step, with
+// arithmetic packed two to an instruction (f32x2); the 16 outputs of a step meet the other
+// n in one butterfly that halves the values a lane carries. The four tokens share one
+// rescaling of the state: with d_s the decay behind token s among the four,
 //   H <- exp(all) H ahead of the first, H <- H + exp(d_s) dt_s x_s B_s^T, y_t = exp(-d_t) H C_t
 // leaves the state itself behind the fourth (d = 0). Where the four decay by more than
-// e^-4 each token rescales as it is written above. Tokens arrive in chunks of kTok through
-// cp.async, two chunks deep.
-// What bounds it: with many units instruction issue and shared memory together (64 x
-// 500 tokens, 24 heads of 64, N = 128: 541 us; 581 us with a rescaling every token; 8 p a
-// thread 566 us, 2 p 706 against 581), with few a warp's own time per token; there the
-// sequence is cut into segments (own end states, a carry, then the outputs), which costs
-// a second pass over x and B.
+// e^-8 they go one by one, by the same code with the others' terms left out. Tokens arrive
+// in chunks of kTok through cp.async, two chunks deep.
+// What bounds it: with many units instruction issue and shared memory together (fp32, 64
+// x 500 tokens, 24 heads of 64, N = 128: 480 us; token by token with a butterfly each 543,
+// with a rescaling each as well 581; 64 columns a CTA 557, 16 517), with few a warp's own
+// time per token; there the sequence is cut into segments (own end states, a carry, then
+// the outputs), which costs a second pass over x and B.
 #include <stdint.h>
 
 #include "ssd_causal.h"
@@ -349,9 +349,9 @@ cudaError_t launch_resolve_slots(const int *slots, int batch, int nslots, int *r
 }
 
 // Segments of at least 64 tokens, as many as it takes to give every SM 16 warps of
-// work (4 x 777 tokens, 8 heads of 128, N = 64: 56 us; with 24 warps 65, 8 warps 71,
-// segments of at least 128 tokens 63; the second and third kernel launched ahead of
-// the one before's end 69).
+// work (4 x 777 tokens, 8 heads of 128, N = 64: 49.5 us; with 24 warps 52, 12 warps 50;
+// segments of at least 48 tokens 47, but one sequence of 100 tokens is then cut in two
+// and takes 12.6 us instead of 7.0).
 void causal_simt_segments(int batch, int L, int H, int P, int N, int sms, int *count, int *tokens) {
     const long long ctas = (long long)batch * H * (P / kCols);
     const long long want = 16LL * sms / (kCols * N / 1024);
