@@ -870,6 +870,20 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         const int wq = warp & 3;
         auto sync_g = [&]() { if (is_b) sync_b(); else sync_a(); };
         const bool whole = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+        // zeros in the output rows that no tile covers, while the first tiles are on their
+        // way: a batch row's by several CTAs (w: batch row and part), or some rows' by one
+        if (p.lens) {
+            const int parts = max(1, (int)gridDim.x / p.batch);
+            const size_t row16 = (size_t)p.HU * 8;       // 16-byte pieces of a token
+            for (long long w = blockIdx.x; w < (long long)p.batch * parts; w += gridDim.x) {
+                const int b = (int)(w / parts), len = p.lens[b];
+                const int covered = len < 0 ? 0 : len == 0 ? kTile : (len + kTile - 1) / kTile * kTile;
+                if (covered >= p.L) continue;
+                uint4 *out = reinterpret_cast<uint4 *>(p.out) + ((size_t)b * p.L + covered) * row16;
+                const size_t n = (size_t)(p.L - covered) * row16, step = (size_t)parts * 256;
+                for (size_t i = (size_t)(w % parts) * 256 + tid - 384; i < n; i += step) out[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
 #pragma unroll 1
         for (uint32_t n = is_b; n < nsteps; n += 2) {
             const uint32_t par = (n >> 1) & 1, nb = n & 1;
@@ -1059,12 +1073,11 @@ __global__ void __launch_bounds__(256) causal_chain_kernel(const TcParams p, int
 }
 
 // What the scan needs ahead of it: its flags cleared and, for a ragged or paged batch
-// (rows not nullptr), resolved pages, effective lengths (-1: skipped) and the zeros of
-// the output rows that no tile covers. Block (b, part).
+// (rows not nullptr), resolved pages and effective lengths (-1: skipped). Block b.
 __global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, int *rows, int *lens, unsigned int *flags, int nflags) {
     const int b = blockIdx.x;
     grid_launch_dependents();
-    if (b == 0 && blockIdx.y == 0)
+    if (b == 0)
         for (int i = threadIdx.x; i < nflags; i += 128) flags[i] = 0u;
     if (!rows) return;
     int row = b;
@@ -1078,18 +1091,11 @@ __global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, in
         bad |= (bool)__syncthreads_or(again);
         if (bad) row = -1;
     }
-    const int len = row < 0 ? -1 : a.len(b);
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
         rows[b] = row;
-        lens[b] = len;
+        lens[b] = row < 0 ? -1 : a.len(b);
         if (bad) atomicOr(&a.status->flags, kFlagIndex);
     }
-    const int covered = len < 0 ? 0 : len == 0 ? kTile : (len + kTile - 1) / kTile * kTile;
-    if (covered >= a.L) return;
-    const size_t row16 = (size_t)a.H * a.P / 8;       // 16-byte pieces of a token
-    uint4 *out = static_cast<uint4 *>(a.out) + ((size_t)b * a.L + covered) * row16;
-    const size_t n = (size_t)(a.L - covered) * row16;
-    for (size_t i = (size_t)blockIdx.y * 128 + threadIdx.x; i < n; i += (size_t)gridDim.y * 128) out[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Scratch of the path behind the status header.
@@ -1183,10 +1189,7 @@ cudaError_t run_tc(const CausalArgs &a, void *scratch, cudaStream_t stream) {
             p.rows = rows;
             p.lens = lens;
         }
-        // enough blocks a row to zero a long tail, few where the rows are many
-        const int parts = 8 * sms / a.batch;
-        const dim3 grid(ragged ? a.batch : 1, !a.seqlens && !a.slots ? 1 : parts < 1 ? 1 : parts > 64 ? 64 : parts);
-        causal_rows_kernel<<<grid, 128, 0, stream>>>(a, ragged ? rows : nullptr, lens, p.flags,
+        causal_rows_kernel<<<ragged ? a.batch : 1, 128, 0, stream>>>(a, ragged ? rows : nullptr, lens, p.flags,
                                                      p.order == kOrderHandoff ? sms : 0);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
