@@ -625,6 +625,12 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 flags = (zero ? kZeroStart : 0) | (w.first ? kFirst : 0) | (w.k + 1 == w.k1 ? kLast : 0) |
                         (st.from_cut ? kFromCut : 0) | (st.to_cut ? kToCut : 0) | (t0 + kTile > len ? kPartial : 0);
                 A_ = A; D_ = D; bias_ = bias;
+                // a unit's start state comes to L2 ahead of the state's warps
+                if (!STATE && p.init && (flags & kFirst) && !(flags & kFromCut)) {
+                    const float *page = p.init + ((size_t)(p.rows ? p.rows[b] : b) * p.HU + hu) * 64 * N;
+#pragma unroll
+                    for (int i = 0; i < 64 * N; i += 32 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(page + i + 32 * lane));
+                }
             }
             if (!had) {
                 if (!there) break;
