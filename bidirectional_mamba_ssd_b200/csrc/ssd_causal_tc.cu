@@ -26,11 +26,11 @@
 //
 // What bounds it: on paper HBM (x, B, C and y once); as measured the work of a tile
 // within an SM. 32 x 1024 tokens, 24 heads of 64, N = 128 (631 MB, 96 us at the rate of
-// a copy): 132 us in a short run at 1.96 GHz, 153 to 163 us in a long one, where the
+// a copy): 132 us in a short run at 1.96 GHz, 157 us in a long one, where the
 // power limit holds the clock near 1.55 GHz. A tile takes an SM about 5500 cycles:
 // nearly 3000 of shared-memory traffic (the MMAs' operands and the terms of diag(w) X),
 // around which mask, state and output have to fit. One sequence of 65536 tokens (1.21
-// GB, 185 us): 418 us, of which the pass for the states 134 and the outputs 250.
+// GB, 185 us): 436 us, of which the pass for the states takes a third.
 //
 // Work is cut so that every CTA has
 // the same number of tiles: the tiles of all units in order, divided evenly. A
