@@ -142,7 +142,7 @@ class Scratch {
             bytes = t.nbytes();
         }
         if (!ok) {
-            PyErr_Clear();
+            if (PyErr_Occurred() && PyErr_ExceptionMatches(PyExc_AttributeError)) PyErr_Clear();    // not an interrupt's
             release();
             throw NotHere();
         }
@@ -223,15 +223,16 @@ PyObject *causal_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         PyObject *init = a[6], *state_out = a[13];
         const auto *lens = (const int *)c.whole(a[7], at::kInt, row), *slots = (const int *)c.whole(a[8], at::kInt, row);
         const auto *bias = (const float *)c.whole(a[9], at::kFloat, vec);
+        const bool paged = a[8] != Py_None;      // (a list of no slots has no address)
         const float lo = (float)number(a[10]), hi = (float)number(a[11]);
         const int path = integer(a[14]);
         at::Tensor state;
-        if (state_out == Py_None && !slots) {
+        if (state_out == Py_None && !paged) {
             state = at::empty({batch, H, P, N}, x.options().dtype(at::kFloat));
         } else {
             if (state_out == Py_None) state_out = init;
             need(state_out != Py_None);
-            state = c.pool(state_out, slots != nullptr, batch, page);
+            state = c.pool(state_out, paged, batch, page);
         }
         const int pages = (int)state.size(0);
         float *start = nullptr;
@@ -279,7 +280,7 @@ PyObject *causal_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const auto *slots = (const int *)c.whole(a[7], at::kInt, row);
         const auto *bias = (const float *)c.whole(a[8], at::kFloat, vec);
         const float lo = (float)number(a[9]), hi = (float)number(a[10]);
-        const at::Tensor &from = c.pool(a[6], slots != nullptr, batch, page);
+        const at::Tensor &from = c.pool(a[6], a[7] != Py_None, batch, page);
         const int pages = (int)from.size(0);
         float *to = (float *)from.data_ptr();
         if (a[12] != Py_None && a[12] != a[6]) {
@@ -317,8 +318,7 @@ const at::Tensor &pages_of(Call &c, PyObject *o, long long *bytes) {
     need(t.dim() >= 3);
     c.lead(o, t.dim());
     need(t.is_contiguous() && t.size(0) <= INT_MAX && t.size(1) <= INT_MAX);
-    *bytes = (long long)t.element_size();
-    for (int64_t i = 2; i < t.dim(); ++i) *bytes *= t.size(i);
+    *bytes = t.numel() ? (long long)(t.nbytes() / (t.size(0) * t.size(1))) : 0;
     return t;
 }
 

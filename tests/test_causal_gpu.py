@@ -589,3 +589,69 @@ def _took(took, name, got):
     if got is not NotImplemented:
         took.append(name)
     return got
+
+
+def test_no_rows_of_a_pool(ssd, monkeypatch):
+    """A batch of no rows with slots: the pool comes back as it is, or, with no pool, the call is refused, either way."""
+    from bidirectional_mamba_ssd_b200 import causal
+    d, t = inputs((0, 5), 2, 64, 64, 1, "f32", seed=1), inputs((0,), 2, 64, 64, 1, "f32", seed=1)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    pool = torch.randn(3, 2, 64, 64, device="cuda")
+    was = pool.clone()
+    for declines in (False, True):
+        if declines:
+            monkeypatch.setattr(causal, "_binding", _Declines)
+        y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], None, pool, slots=none)
+        assert y.shape == (0, 5, 2, 64) and h is pool
+        assert ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], None, pool, none).shape == (0, 2, 64)
+        with pytest.raises(ValueError):
+            ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], slots=none)
+        with pytest.raises((TypeError, ValueError)):
+            ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], None, pool)
+    assert torch.equal(pool, was)
+
+
+def test_workspaces_of_the_binding(ssd):
+    """A workspace that has yet to be made, one that is too small, one of something else, and one whose lock is held."""
+    import threading
+    d = inputs((2, 300), 2, 64, 64, 1, "bf16", seed=3)
+    call = lambda ws: ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], workspace=ws)  # noqa: E731
+    want = call(None)[0]
+    ws = ssd.Workspace(torch.device("cuda", 0))
+    assert torch.equal(call(ws)[0], want)
+    ws.buf = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert torch.equal(call(ws)[0], want) and ws.buf.numel() > 256
+    with pytest.raises(AttributeError):
+        call(object())
+    got = []
+    with ws.lock:
+        th = threading.Thread(target=lambda: got.append(call(ws)[0]))
+        th.start()
+        th.join(0.2)
+        assert not got
+    th.join()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and ws.status() == 0
+
+
+def test_first_call_of_a_thread(ssd):
+    """A thread whose first CUDA call this is, of each operator: there is no current context yet."""
+    import threading
+    d, t = inputs((2, 300), 2, 64, 64, 1, "bf16", seed=3), inputs((2,), 2, 64, 64, 1, "bf16", seed=4)
+    pool = torch.randn(1, 4, 2, 64, 64, device="cuda")
+    idx = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    z = si.bidir_inputs(8, 300, 24, 64, 128, 24, "bf16", seed=5, device="cuda")
+    both = [z[k] for k in ("x", "dt", "A", "B", "C", "D")]
+    calls = [lambda: ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"])[0],
+             lambda: ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], path=ssd.SSD_PATH_SIMT)[0],
+             lambda: ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], None, pool[0].clone(), idx),
+             lambda: ssd.ssd_cache_copy(pool.clone(), idx, idx + 1), lambda: ssd.ssd_cache_compact(pool.clone(), idx)[0],
+             lambda: ssd.ssd_bidir_fwd(*both)]
+    for k, call in enumerate(calls):
+        want, got = call(), []
+        torch.cuda.synchronize()
+        th = threading.Thread(target=lambda: got.append(call()))
+        th.start()
+        th.join()
+        torch.cuda.synchronize()
+        assert got and torch.equal(got[0], want), f"call {k}"
