@@ -88,7 +88,7 @@ struct SimtSmem {
 constexpr float kMaxQuad = 8.f;
 
 template <typename T, int N, int COLS, int MODE>
-__global__ void __launch_bounds__(COLS *N / (8 * KP))
+__global__ void __launch_bounds__(COLS *N / (8 * KP), 1)
 causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     constexpr int THREADS = COLS * N / (8 * KP);
     constexpr int NG = N / 8;                 // lanes that share a column
@@ -326,17 +326,22 @@ __global__ void __launch_bounds__(256) causal_carry_kernel(const CausalArgs a, c
     }
 }
 
-constexpr int kCols = 32;   // columns of a CTA
+// Columns of a CTA: 128 threads. fp32, 32 and 64 columns: 4 x 777 tokens, 8 heads of
+// 128, N = 64 49.5 and 46.9 us, 100 x 300 tokens 184 and 175; N = 128, 64 x 500 tokens, 24
+// heads of 64 479 and 557. (With the registers that a kernel without a bound on its CTAs
+// gets, 32 columns of N = 128 and 64 of N = 64 take 483, 50.2 and 165.)
+constexpr int cols_of(int N) { return 4096 / N; }
 
 template <typename T, int N>
 cudaError_t run_simt(const CausalArgs &a, const CausalSegments &s, int mode, cudaStream_t stream) {
-    const long long grid = (long long)a.batch * a.H * s.count * (a.P / kCols);
+    constexpr int COLS = cols_of(N);
+    const long long grid = (long long)a.batch * a.H * s.count * (a.P / COLS);
     if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
-    const int threads = kCols * N / (8 * KP);
-    const size_t smem = sizeof(SimtSmem<T, N, kCols>);
-    static_assert(sizeof(SimtSmem<T, N, kCols>) <= 48 * 1024, "shared memory within the default limit");
-    if (mode == kCausalOutput) causal_simt_kernel<T, N, kCols, kCausalOutput><<<(unsigned)grid, threads, smem, stream>>>(a, s);
-    else causal_simt_kernel<T, N, kCols, kCausalState><<<(unsigned)grid, threads, smem, stream>>>(a, s);
+    const int threads = COLS * N / (8 * KP);
+    const size_t smem = sizeof(SimtSmem<T, N, COLS>);
+    static_assert(sizeof(SimtSmem<T, N, COLS>) <= 48 * 1024, "shared memory within the default limit");
+    if (mode == kCausalOutput) causal_simt_kernel<T, N, COLS, kCausalOutput><<<(unsigned)grid, threads, smem, stream>>>(a, s);
+    else causal_simt_kernel<T, N, COLS, kCausalState><<<(unsigned)grid, threads, smem, stream>>>(a, s);
     return cudaGetLastError();
 }
 
@@ -349,12 +354,13 @@ cudaError_t launch_resolve_slots(const int *slots, int batch, int nslots, int *r
 }
 
 // Segments of at least 64 tokens, as many as it takes to give every SM 16 warps of
-// work (4 x 777 tokens, 8 heads of 128, N = 64: 49.5 us; with 24 warps 52, 12 warps 50;
-// segments of at least 48 tokens 47, but one sequence of 100 tokens is then cut in two
+// work (4 x 777 tokens, 8 heads of 128, N = 64, at 32 columns: 49.5 us; with 24 warps 52,
+// 12 warps 50; segments of at least 48 tokens 47, but one sequence of 100 tokens is then cut in two
 // and takes 12.6 us instead of 7.0).
 void causal_simt_segments(int batch, int L, int H, int P, int N, int sms, int *count, int *tokens) {
-    const long long ctas = (long long)batch * H * (P / kCols);
-    const long long want = 16LL * sms / (kCols * N / 1024);
+    const int cols = cols_of(N);
+    const long long ctas = (long long)batch * H * (P / cols);
+    const long long want = 16LL * sms / (cols * N / 1024);
     long long n = ctas > 0 ? want / ctas : 1;
     const long long most = L / 64;
     n = n < most ? n : most;
