@@ -13,11 +13,17 @@
 //   exp(a_t - a_s) = exp(a_t - a_r) * exp(a_r - a_s)
 // so that M needs one factor per column, c_s = exp(a_r - a_s) dt_s, and the row's
 // factor exp(a_t - a_r) is applied to the fp32 result. With a_r half the tile's decay
-// both stay within e^+-75 while that is at most 150; C H is taken of exp(a_r) H and
+// both stay within e^+-40 while that is at most 80; C H is taken of exp(a_r) H and
 // adds up with M X in one accumulator. Past that (a test on the tile) the rows of each
 // half of the tile have a reference of their own, half way through their half, and the
-// columns a factor for each, up to a decay of 150 in a half; past that each entry takes
+// columns a factor for each, up to a decay of 80 in a half; past that each entry takes
 // its own exponential. In both C H has an accumulator of its own.
+// The span is a choice about range: M, exp(a_r) H and the sums of M X carry a factor of up
+// to e^+-40 = 2.4e+-17 inside bf16's and fp32's 1.2e-38 .. 3.4e38, which leaves the terms
+// G dt x and C H that enter an output 1e-20 .. 1e20 (e^+-75 would leave 4e-6 .. 9e5, which
+// activations do reach). With a reference a half, terms that have decayed by more than e^-47 =
+// 4e-21 may come out as zero. 32 x 1024 tokens, 24 heads of 64, every tile decaying by 20, 100, 200,
+// 320: 132, 131, 143, 155 us (one factor, two, an exponential an entry for the last two).
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
 // products whose result is rounded to bf16 (relative 2^-9 a term, random). The
@@ -76,7 +82,7 @@ constexpr int kThreads = 640;
 constexpr int kStateThreads = 384;    // without the output groups
 constexpr int kVec = 4;               // tiles whose decays are kept
 constexpr uint32_t kHalf = 8192;      // 64 rows x 128 bytes
-constexpr float kMaxSpan = 150.f;     // decay up to which a tile's, or a half tile's, mask has one factor per column
+constexpr float kMaxSpan = 80.f;      // decay up to which a tile's, or a half tile's, mask has one factor per column
 
 // A run of work of one CTA: n units from u0 on, of each the tiles [k0, k1) (k1 < 0:
 // all). from_cut: the state entering comes from the CTA before; to_cut: the state

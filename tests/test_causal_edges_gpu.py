@@ -1,0 +1,71 @@
+"""GPU tests of the causal serving operators at the edges of what a call may be
+given, against the recurrence in 64 bits (causal_ref), at the tolerances of
+test_causal_gpu where a test derives none of its own."""
+import numpy as np
+import pytest
+import torch
+
+import causal_ref as ref
+from test_causal_gpu import check_state, inputs, sizes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import bidirectional_mamba_ssd_b200 as m
+    return m
+
+
+def rounding_bound(x, dt, A, B, C, h0, y, o):
+    """How far one row's bf16 outputs y (L, H, P) may be from the exact o, element by element, without a skip term.
+
+    A tile of 128 tokens from the state H entering it: y_t = sum_s G_ts e_ts dt_s x_s + e_t C_t H. The kernel rounds G e dt
+    and H to bf16 (2^-8 of each at most) and the output (half a step). The rest is fp32: exponents up to 320 that are sums of
+    128 step sizes (each addition off by 2^-24 of up to 320: 8 additions a sum are 1.6e-4 = 2^-12.6, and a difference of two
+    twice that), and sums of 256 products (256 x 2^-23 = 2^-15 of the products' magnitudes). So, with E the sum of the
+    magnitudes of the terms and F the same with every product of C and B by itself,
+        |y - o| <= (2^-8 + 2^-11) E + 2^-14 F + half a step of the output."""
+    x, dt, A, B, C, h = (t.double().cpu() for t in (x, dt, A, B, C, h0))
+    L, H, _ = x.shape
+    group = torch.arange(H) // (H // B.shape[1])
+    E, F = torch.zeros_like(x), torch.zeros_like(x)
+    for t0 in range(0, L, 128):
+        t1 = min(L, t0 + 128)
+        xs, Bs, Cs, ds = x[t0:t1].transpose(0, 1), B[t0:t1, group].transpose(0, 1), C[t0:t1, group].transpose(0, 1), dt[t0:t1].T
+        a = torch.cumsum(ds * A[:, None], 1)
+        e = torch.exp((a[:, :, None] - a[:, None, :]).masked_fill(~torch.ones(t1 - t0, t1 - t0, dtype=bool).tril(), -np.inf))
+        w, in_ = e * ds[:, None, :], torch.exp(a)[:, :, None]
+        at_start = in_ * (Cs.abs() @ h.abs().transpose(1, 2))
+        E[t0:t1] = ((((Cs @ Bs.transpose(1, 2)).abs() * w) @ xs.abs()) + at_start).transpose(0, 1)
+        F[t0:t1] = ((((Cs.abs() @ Bs.abs().transpose(1, 2)) * w) @ xs.abs()) + at_start).transpose(0, 1)
+        h = torch.exp(a[:, -1])[:, None, None] * h + ((ds * torch.exp(a[:, -1:] - a))[:, :, None] * xs).transpose(1, 2) @ Bs
+    top = torch.maximum(y.abs(), o.abs()).clamp(min=2.0 ** -126)
+    return (2 ** -8 + 2 ** -11) * E + 2 ** -14 * F + 0.5 * torch.exp2(torch.floor(torch.log2(top)) - 7)
+
+
+# factors on x (and the start state), on B and on C, of the usual inputs (1, 1/8, 1/8)
+SCALES = [(1.0, 1.0), (1e-15, 1.0), (1e-8, 1.0), (1e-7, 1.0), (1e4, 80.0), (500.0, 400.0), (1e12, 8.0)]
+
+
+@pytest.mark.parametrize("scale", SCALES, ids=lambda s: "x%g_bc%g" % s)
+def test_fwd_decays_at_any_magnitude(ssd, scale):
+    """A tile of 128 tokens decays by e^-60 to e^-320, both sides of the spans where the masked matrix changes its
+    references among them, with inputs and start states of any magnitude and no skip term."""
+    spans = [60.0, 79.5, 80.5, 120.0, 149.8, 159.0, 161.0, 320.0]
+    d = inputs((1, 300), len(spans), 64, 128, 2, "bf16", seed=41)
+    d["dt"].fill_(0.1)
+    A = -torch.tensor(spans, device="cuda") / (128 * d["dt"][0, 0, 0].float())
+    x, B, C = d["x"] * scale[0], d["B"] * scale[1], d["C"] * scale[1]
+    h0 = torch.randn(1, len(spans), 64, 128, generator=d["g"], device="cuda") * scale[0]
+    o, oh = ref.fwd(x, sizes(d), A, B, C, None, h0, [300])
+    assert np.isfinite(o.to(torch.bfloat16).float().numpy()).all()
+    y, h = ssd.ssd_causal_fwd(x, d["dt"], A, B, C, None, h0)
+    torch.cuda.synchronize()
+    assert ssd.ssd_get_device_status() == 0
+    y = y.double().cpu()
+    assert torch.isfinite(y).all(), [s for k, s in enumerate(spans) if not torch.isfinite(y[:, :, k]).all()]
+    off = (y - o).abs()[0] / rounding_bound(x[0], sizes(d)[0], A, B[0], C[0], h0[0], y[0], o[0])
+    for k, s in enumerate(spans):
+        assert off[:, k].max() <= 1, f"decay {s}: {off[:, k].max():.2f} of the bound"
+        check_state(h[:, k], oh[:, k], f"decay {s}")
