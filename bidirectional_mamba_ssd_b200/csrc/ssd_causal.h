@@ -23,7 +23,8 @@ struct StepSize {
     // the same with the head's bias at hand
     __device__ __forceinline__ float with(float v, float b) const {
         if (!bias) return v;
-        return fminf(fmaxf(softplus(v + b), lo), hi);
+        const float s = softplus(v + b);
+        return s < lo ? lo : s > hi ? hi : s;      // (fminf and fmaxf would make a limit of a NaN)
     }
 };
 

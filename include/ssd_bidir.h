@@ -411,7 +411,8 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
  *    overlap. Pages that no row names are left as they were.
  *  - dt_bias NULL: dt is the step size. Otherwise it is the raw projection and
  *    the step size min(max(softplus(dt + dt_bias[h]), dt_min), dt_max), as for
- *    ssd_bidir_fwd_dtraw, kept in fp32. D may be NULL (no skip term).
+ *    ssd_bidir_fwd_dtraw, kept in fp32; a NaN stays a NaN (there it becomes
+ *    dt_min). D may be NULL (no skip term).
  *  - A <= 0 and step sizes >= 0, as above; device memory is not checked for it.
  *  - Forward only: there is no backward pass of these calls. */
 

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import causal_ref as ref
-from test_causal_gpu import check_state, inputs, sizes
+from test_causal_gpu import check_state, inputs, paths_of, sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,27 @@ def test_fwd_decays_at_any_magnitude(ssd, scale):
     for k, s in enumerate(spans):
         assert off[:, k].max() <= 1, f"decay {s}: {off[:, k].max():.2f} of the bound"
         check_state(h[:, k], oh[:, k], f"decay {s}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("hi", [0.1, float("inf")])
+def test_nan_in_a_raw_step_size_shows(ssd, io, hi):
+    """A raw step size of NaN makes its head's outputs from there on, and its state, NaN; other heads are as they were."""
+    d = inputs((2, 300), 3, 64, 64, 1, io, seed=42, raw=True)
+    kw = dict(dt_bias=d["dt_bias"], dt_min=0.0, dt_max=hi)
+    bad = d["dt"].clone()
+    bad[1, 200, 1] = float("nan")
+    a = [d[k] for k in ("A", "B", "C", "D")]
+    for path in paths_of(ssd, io):
+        y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], *a, path=path, **kw)
+        z, g = ssd.ssd_causal_fwd(d["x"], bad, *a, path=path, **kw)
+        torch.cuda.synchronize()
+        assert torch.isnan(z[1, 200:, 1]).all() and torch.isnan(g[1, 1]).all(), f"path {path}"
+        for b, k in ((0, 0), (0, 1), (0, 2), (1, 0), (1, 2)):
+            assert torch.equal(z[b, :, k], y[b, :, k]) and torch.equal(g[b, k], h[b, k]), f"path {path}"
+    t = [v[:, 200].contiguous() for v in (d["x"], bad, d["B"], d["C"])]
+    st = torch.zeros(2, 3, 64, 64, device="cuda")
+    y = ssd.ssd_causal_step(t[0], t[1], d["A"], t[2], t[3], d["D"], st, **kw)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[1, 1]).all() and torch.isnan(st[1, 1]).all()
+    assert torch.isfinite(y[0]).all() and torch.isfinite(st[0]).all() and torch.isfinite(y[1, [0, 2]]).all()
