@@ -107,7 +107,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.buf = None
-        self.lock = threading.Lock()   # held by calls that make several launches on the buffer
+        self.lock = threading.Lock()   # held by every call from get() to its last launch: threads on one stream take turns
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
@@ -172,10 +172,11 @@ def ssd_bidir_fwd(x, dt, A, B, C, D, out=None, *, chunk: int = 256, path: int = 
     nbytes = ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, chunk, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_bidir_fwd")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_bidir_fwd_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out),
-                                batch, L, H, P, N, G, chunk, _DT[io], int(path),
-                                _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_bidir_fwd_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out),
+                                    batch, L, H, P, N, G, chunk, _DT[io], int(path),
+                                    _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_bidir_fwd")
     return out
 
@@ -211,10 +212,11 @@ def ssd_prefix_state(x, dt, A, B, init=None, out=None, *, chunk: int = 256, path
     nbytes = ssd_workspace_bytes(SSD_OP_PREFIX_STATE, batch, L, H, P, N, G, chunk, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_prefix_state")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_prefix_state_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(init), _ptr(out),
-                                   batch, L, H, P, N, G, chunk, _DT[io], int(path),
-                                   _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_prefix_state_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(init), _ptr(out),
+                                       batch, L, H, P, N, G, chunk, _DT[io], int(path),
+                                       _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_prefix_state")
     return out
 
@@ -253,10 +255,11 @@ def ssd_prefix_state_layers(x, dt, A, B, init=None, out=None, *, chunk: int = 25
     nbytes = ssd_workspace_bytes(SSD_OP_PREFIX_STATE, layers * batch, L, H, P, N, G, chunk, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_prefix_state_layers")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_prefix_state_layers(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(init), _ptr(out),
-                                     layers, batch, L, H, P, N, G, chunk, _DT[io],
-                                     _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_prefix_state_layers(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(init), _ptr(out),
+                                         layers, batch, L, H, P, N, G, chunk, _DT[io],
+                                         _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_prefix_state_layers")
     return out
 
@@ -292,10 +295,11 @@ def ssd_block_step(x, dt, A, B, C, D, prefix_state, out=None, *, path: int = SSD
     nbytes = ssd_workspace_bytes(SSD_OP_BLOCK_STEP, batch, T, H, P, N, G, 64, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_block_step")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_block_step_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                 _ptr(prefix_state), _ptr(out), batch, T, H, P, N, G, _DT[io],
-                                 int(path), _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_block_step_path(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                     _ptr(prefix_state), _ptr(out), batch, T, H, P, N, G, _DT[io],
+                                     int(path), _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_block_step")
     return out
 
@@ -337,9 +341,10 @@ def ssd_segment_states(x, dt, A, B, *, workspace: Workspace | None = None):
     rd = torch.empty_like(fd)
     stream = _stream(dev)
     ws = _workspace(dev, stream, workspace)
-    buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
-    rc = lib.ssd_segment_states(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(fs), _ptr(fd), _ptr(rs), _ptr(rd),
-                                batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
+        rc = lib.ssd_segment_states(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(fs), _ptr(fd), _ptr(rs), _ptr(rd),
+                                    batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_segment_states")
     return fs, fd, rs, rd
 
@@ -378,10 +383,11 @@ def ssd_bidir_fwd_seeded(x, dt, A, B, C, D, fwd_init=None, rev_init=None, out=No
             raise ValueError("out must have x's shape")
     stream = _stream(dev)
     ws = _workspace(dev, stream, workspace)
-    buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
-    rc = lib.ssd_bidir_fwd_seeded(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(fwd_init),
-                                  _ptr(rev_init), _ptr(out), batch, L, H, P, N, G, _DT[io],
-                                  _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
+        rc = lib.ssd_bidir_fwd_seeded(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(fwd_init),
+                                      _ptr(rev_init), _ptr(out), batch, L, H, P, N, G, _DT[io],
+                                      _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_bidir_fwd_seeded")
     return out
 
@@ -403,10 +409,11 @@ def ssd_bidir_fwd_dtraw(x, dt_raw, dt_bias, A, B, C, D, dt_min: float = 0.0, dt_
             raise ValueError("out must have x's shape")
     stream = _stream(dev)
     ws = _workspace(dev, stream, workspace)
-    buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
-    rc = lib.ssd_bidir_fwd_dtraw(_ptr(x), _ptr(dt_raw), _ptr(dt_bias), float(dt_min), float(dt_max),
-                                 _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out), batch, L, H, P, N, G, _DT[io],
-                                 _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(max(ssd_workspace_bytes(SSD_OP_BIDIR_FWD, batch, L, H, P, N, G, 64, io), 256))
+        rc = lib.ssd_bidir_fwd_dtraw(_ptr(x), _ptr(dt_raw), _ptr(dt_bias), float(dt_min), float(dt_max),
+                                     _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out), batch, L, H, P, N, G, _DT[io],
+                                     _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_bidir_fwd_dtraw")
     return out
 
@@ -451,13 +458,14 @@ def ssd_bidir_bwd(x, dt, A, B, C, D, dy, *, fwd_init=None, rev_init=None,
     nbytes = ssd_workspace_bytes(SSD_OP_BIDIR_BWD, batch, L, H, P, N, G, 64, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_bidir_bwd")
-    buf = ws.get(nbytes)
-    opt = lambda t: _ptr(t) if t is not None else None
-    rc = lib.ssd_bidir_bwd_seeded(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), opt(fwd_init),
-                                  opt(rev_init), _ptr(dy),
-                                  *(_ptr(g[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD")),
-                                  opt(g.get("d_fwd_init")), opt(g.get("d_rev_init")),
-                                  batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        opt = lambda t: _ptr(t) if t is not None else None
+        rc = lib.ssd_bidir_bwd_seeded(_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), opt(fwd_init),
+                                      opt(rev_init), _ptr(dy),
+                                      *(_ptr(g[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD")),
+                                      opt(g.get("d_fwd_init")), opt(g.get("d_rev_init")),
+                                      batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_bidir_bwd")
     return g
 
@@ -498,9 +506,10 @@ def ssd_bidir_fwd_x2(x2, dt, A, B, C, D, out=None, *, workspace: Workspace | Non
     nbytes = ssd_workspace_bytes(SSD_OP_BIDIR_FWD_X2, batch, L, H, P, N, G, 64, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_bidir_fwd_x2")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_bidir_fwd_x2(_ptr(x2), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out),
-                              batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_bidir_fwd_x2(_ptr(x2), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(out),
+                                  batch, L, H, P, N, G, _DT[io], _ptr(buf), buf.numel(), ctypes.c_void_p(stream))
     _check(rc, "ssd_bidir_fwd_x2")
     return out
 
@@ -538,11 +547,12 @@ def ssd_mixer_block_fwd(xbc, z, dt_raw, conv_w, conv_b, dt_bias, A, D, norm_w, n
     nbytes = ssd_workspace_bytes(SSD_OP_MIXER_BLOCK, batch, L, nheads, P, dstate, ngroups, 64, io)
     if nbytes == 0:
         _check(_c.SSD_ERR_UNSUPPORTED, "ssd_mixer_block_fwd")
-    buf = ws.get(nbytes)
-    rc = lib.ssd_mixer_block_fwd(_ptr(xbc), _ptr(z), _ptr(dt_raw), _ptr(conv_w), _ptr(conv_b), K, _ptr(dt_bias),
-                                 float(dt_min), float(dt_max), _ptr(A), _ptr(D), _ptr(norm_w), float(norm_eps),
-                                 _ptr(out), batch, L, nheads, P, dstate, ngroups, _DT[io], _ptr(buf), buf.numel(),
-                                 ctypes.c_void_p(stream))
+    with ws.lock:
+        buf = ws.get(nbytes)
+        rc = lib.ssd_mixer_block_fwd(_ptr(xbc), _ptr(z), _ptr(dt_raw), _ptr(conv_w), _ptr(conv_b), K, _ptr(dt_bias),
+                                     float(dt_min), float(dt_max), _ptr(A), _ptr(D), _ptr(norm_w), float(norm_eps),
+                                     _ptr(out), batch, L, nheads, P, dstate, ngroups, _DT[io], _ptr(buf), buf.numel(),
+                                     ctypes.c_void_p(stream))
     _check(rc, "ssd_mixer_block_fwd")
     return out
 

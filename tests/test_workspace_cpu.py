@@ -1,0 +1,56 @@
+"""Host-only checks of the Workspace class and of who holds its lock (nothing is
+launched: the library's calls are replaced by recorders)."""
+import pytest
+import torch
+
+import bidirectional_mamba_ssd_b200 as ssd
+
+B, L, H, P, N, G = 2, 8, 2, 64, 64, 1
+
+
+def calls(ws):
+    """Every entry point that takes a workspace and is called over ctypes, with small CPU tensors."""
+    io = torch.bfloat16
+    z = lambda *s: torch.zeros(*s, dtype=io)  # noqa: E731
+    f = lambda *s: torch.zeros(*s)  # noqa: E731
+    x, dt, bc, A = z(B, L, H, P), z(2, B, L, H), z(2, B, L, G, N), f(2, H)
+    layers = (x[None], dt[:1], A[:1], bc[:1])
+    cin = H * P + 2 * G * N
+    block = (z(B, L, cin), x, dt, f(2, cin, 4), f(2, cin), A, A, A, f(H * P))
+    return {
+        "ssd_bidir_fwd": lambda: ssd.ssd_bidir_fwd(x, dt, A, bc, bc, A, workspace=ws),
+        "ssd_bidir_bwd": lambda: ssd.ssd_bidir_bwd(x, dt, A, bc, bc, A, x, workspace=ws),
+        "ssd_block_step_bwd": lambda: ssd.ssd_block_step_bwd(x, dt, A, bc, bc, A, None, x, workspace=ws),
+        "ssd_bidir_fwd_x2": lambda: ssd.ssd_bidir_fwd_x2(torch.stack([x, x]), dt, A, bc, bc, A, workspace=ws),
+        "ssd_prefix_state": lambda: ssd.ssd_prefix_state(x, dt[0], A[0], bc[0], workspace=ws),
+        "ssd_prefix_state_layers": lambda: ssd.ssd_prefix_state_layers(*layers, workspace=ws),
+        "ssd_block_step": lambda: ssd.ssd_block_step(x, dt, A, bc, bc, A, None, workspace=ws),
+        "ssd_segment_states": lambda: ssd.ssd_segment_states(x, dt, A, bc, workspace=ws),
+        "ssd_bidir_fwd_seeded": lambda: ssd.ssd_bidir_fwd_seeded(x, dt, A, bc, bc, A, workspace=ws),
+        "ssd_bidir_fwd_dtraw": lambda: ssd.ssd_bidir_fwd_dtraw(x, dt, A, A, bc, bc, A, workspace=ws),
+        "ssd_mixer_block_fwd": lambda: ssd.ssd_mixer_block_fwd(*block, H, G, N, workspace=ws),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(calls(None)))
+def test_every_call_holds_its_workspace(monkeypatch, name):
+    """A call's launches share the workspace's buffer: its lock is held from the buffer's choice to the last launch, so that
+    no other thread's call on the same stream comes between them."""
+    ws = ssd.Workspace("cpu")
+    made = []
+
+    class Lib:
+        ssd_workspace_bytes = staticmethod(lambda *a: 4096)
+
+        def __getattr__(self, entry):
+            def call(*a):
+                made.append((entry, ws.lock.locked()))
+                return 0
+            return call
+
+    monkeypatch.setattr(ssd, "lib", Lib())
+    monkeypatch.setattr(ssd, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(ssd, "_stream", lambda device: 0)
+    calls(ws)[name]()
+    assert made and all(held for _, held in made), made
+    assert not ws.lock.locked()
