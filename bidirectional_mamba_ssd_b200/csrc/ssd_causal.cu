@@ -110,9 +110,10 @@ causal_simt_kernel(const CausalArgs a, const CausalSegments sg) {
     T *out = static_cast<T *>(a.out) + ((size_t)b * a.L * a.H + h) * a.P + part * COLS;   // + t H P
     // zero rows [t, stop): behind the sequence, or the whole row of a skipped one
     auto blank = [&](int t) {
-        const int chunks = COLS * (int)sizeof(T) / 16;
-        for (int i = t * chunks + tid; i < stop * chunks; i += THREADS)
-            reinterpret_cast<uint4 *>(out + (size_t)(i / chunks) * a.H * a.P)[i % chunks] = make_uint4(0, 0, 0, 0);
+        constexpr int PIECES = COLS * (int)sizeof(T) / 16;
+        static_assert(THREADS % PIECES == 0, "whole rows at a step");
+        for (int r = t + tid / PIECES; r < stop; r += THREADS / PIECES)
+            reinterpret_cast<uint4 *>(out + (size_t)r * a.H * a.P)[tid % PIECES] = make_uint4(0, 0, 0, 0);
     };
     if (row < 0) {
         if (OUT) blank(first);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import causal_ref as ref
-from test_causal_gpu import check_state, inputs, paths_of, sizes
+from test_causal_gpu import check_out, check_state, inputs, paths_of, sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,30 @@ def test_nan_in_a_raw_step_size_shows(ssd, io, hi):
     torch.cuda.synchronize()
     assert torch.isnan(y[1, 1]).all() and torch.isnan(st[1, 1]).all()
     assert torch.isfinite(y[0]).all() and torch.isfinite(st[0]).all() and torch.isfinite(y[1, [0, 2]]).all()
+
+
+@pytest.mark.parametrize("io,path", [("f32", "SIMT"), ("bf16", "SIMT"), ("bf16", "AUTO")])
+def test_rows_behind_a_sequence_past_31_bits(ssd, io, path):
+    """A padded sequence of so many rows that its 16-byte pieces do not count in 31 bits: all rows behind its 300 tokens
+    are zero. (x, B and C are one array, of which only the tokens are ever set.)"""
+    torch.cuda.empty_cache()
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[io]
+    L, lens = 2 ** 31 * 16 // (64 * dtype.itemsize) + 1000, 300
+    if torch.cuda.mem_get_info()[0] < 2 * L * 64 * dtype.itemsize + (8 << 30):
+        pytest.skip("not enough free memory")
+    d = inputs((1, lens), 1, 64, 64, 1, io, seed=70)
+    x = torch.empty(1, L, 1, 64, dtype=dtype, device="cuda")
+    dt = torch.empty(1, L, 1, dtype=dtype, device="cuda")
+    x[:, :lens], dt[:, :lens] = d["x"], d["dt"]
+    out = torch.full_like(x, 7.0)
+    seqlens = torch.tensor([lens], dtype=torch.int32, device="cuda")
+    y, h = ssd.ssd_causal_fwd(x, dt, d["A"], x, x, d["D"], seqlens=seqlens, out=out, path=getattr(ssd, "SSD_PATH_" + path))
+    torch.cuda.synchronize()
+    assert ssd.ssd_get_device_status() == 0
+    for part in y.view(-1)[lens * 64:].split(1 << 28):
+        assert not part.any()
+    o, oh = ref.fwd(d["x"], sizes(d), d["A"], d["x"], d["x"], d["D"], torch.zeros(1, 1, 64, 64), [lens])
+    check_out(y[:, :lens], o, io, path)
+    check_state(h, oh, path)
+    del x, out, y, dt
+    torch.cuda.empty_cache()
