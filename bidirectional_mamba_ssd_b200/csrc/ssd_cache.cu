@@ -392,16 +392,17 @@ cache_compact_kernel(const CacheArgs a) {
     }
 }
 
-// Shared memory and grid: with bulk copies one CTA per SM, else eight.
-template <typename V, typename K>
-cudaError_t launch(K kernel, const CacheArgs &a, long long pairs, size_t maps, cudaStream_t stream) {
+// Shared memory (MAPS maps of a word for 32 slots) and grid: with bulk copies one CTA per SM, else eight.
+template <typename V, int MAPS, typename K>
+cudaError_t launch(K kernel, const CacheArgs &a, long long pairs, cudaStream_t stream) {
     constexpr bool kBulk = sizeof(V) == 16;
-    const size_t smem = maps + (kBulk ? sizeof(BulkSmem) : 0);
-    cudaError_t e;
-    if (smem > 40 * 1024 &&
-        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return e;
-    static_assert(!kBulk || sizeof(BulkSmem) + kCacheMaxSlots / 32 * 8 <= 232448 - 2048, "stages and maps in shared memory");
+    constexpr size_t kStaged = kBulk ? sizeof(BulkSmem) : 0, kMost = kStaged + kCacheMaxSlots / 32 * 4 * MAPS;
+    static_assert(kMost <= 232448 - 2048, "stages and maps in shared memory");
+    const size_t smem = kStaged + (size_t)((a.nslots + 31) / 32) * 4 * MAPS;
+    // the limit belongs to the kernel, not to the launch: always the largest pool's, or another
+    // thread's call on a smaller pool could lower it ahead of this launch
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    if (e != cudaSuccess) return e;
     const long long per = kBulk ? (a.page_bytes + kPiece - 1) / kPiece * pairs
                                 : (a.page_bytes / (long long)sizeof(V) + kThreads - 1) / kThreads * ((pairs + kGroup - 1) / kGroup);
     const long long items = per * a.layers, most = (kBulk ? 1LL : 8LL) * device_sms();
@@ -410,13 +411,13 @@ cudaError_t launch(K kernel, const CacheArgs &a, long long pairs, size_t maps, c
 }
 template <typename V>
 cudaError_t copy_v(const CacheArgs &a, cudaStream_t stream) {
-    return launch<V>(cache_copy_kernel<V>, a, a.n, (size_t)((a.nslots + 31) / 32) * 4, stream);
+    return launch<V, 1>(cache_copy_kernel<V>, a, a.n, stream);
 }
 template <typename V>
 cudaError_t compact_v(const CacheArgs &a, cudaStream_t stream) {
     // no more moves than half the pages or than rows of the table
     const long long moves = a.rows < a.nslots / 2 ? a.rows : a.nslots / 2;
-    return launch<V>(cache_compact_kernel<V>, a, moves, (size_t)((a.nslots + 31) / 32) * 8, stream);
+    return launch<V, 2>(cache_compact_kernel<V>, a, moves, stream);
 }
 
 int width(const CacheArgs &a) {

@@ -1,6 +1,9 @@
 """GPU tests of the causal serving operators at the edges of what a call may be
 given, against the recurrence in 64 bits (causal_ref), at the tolerances of
 test_causal_gpu where a test derives none of its own."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -120,3 +123,34 @@ def test_rows_behind_a_sequence_past_31_bits(ssd, io, path):
     check_state(h, oh, path)
     del x, out, y, dt
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("width", [4, 1])
+def test_pools_of_two_sizes_at_once(ssd, width):
+    """Copies and compactions of large and of small pools from four threads, on streams and workspaces of their own: the
+    kernels' shared memory depends on the number of slots. (Through the C ABI, which gives the other threads the most time
+    between a call's steps.)"""
+    v, refused = ctypes.c_void_p, []
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def work(nslots, number):
+        pool = torch.full((1, nslots, width), float(number), device="cuda")
+        pool[0, 2:] = 0.0
+        stream, src, dst, live = torch.cuda.Stream(), i32(0, 1), i32(2, 3), i32(0)
+        ws, new = torch.zeros(256, dtype=torch.uint8, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        head, tail = (v(pool.data_ptr()), 4 * width, 1, nslots), (v(ws.data_ptr()), 256, v(stream.cuda_stream))
+        copy = (*head, v(src.data_ptr()), v(dst.data_ptr()), 2, *tail)
+        compact = (*head, v(src.data_ptr()), 2, v(new.data_ptr()), v(live.data_ptr()), *tail)
+        for i in range(4000):
+            rc = ssd.lib.ssd_cache_copy(*copy), ssd.lib.ssd_cache_compact(*compact)
+            if rc != (0, 0):
+                refused.append((nslots, i, rc))
+        stream.synchronize()
+        if not (pool[0, :4] == number).all() or pool[0, 4:].any() or live.item() != 2 or new.tolist() != [0, 1]:
+            refused.append((nslots, "pages"))
+
+    ts = [threading.Thread(target=work, args=a) for a in ((200000, 1), (4, 2), (262144, 3), (4, 4))]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not refused, (len(refused), refused[:3])
