@@ -133,10 +133,25 @@ def _workspace(device, stream, ws):
     return _default_ws[key]
 
 
+_captured: set = set()      # devices on which calls without a workspace have been captured
+
+
+def _captured_header() -> int:
+    """The address of the library's own status header on the current device (include/ssd_bidir.h: ssd_captured_status)."""
+    p = ctypes.c_void_p()
+    _check(lib.ssd_captured_status(ctypes.byref(p)), "ssd_captured_status")
+    return p.value
+
+
 def ssd_get_device_status(ws: Workspace | None = None) -> int:
+    """Synchronise the current stream; read and clear the status of a workspace, or of the stream's own and then of the
+    serving calls (causal.py) that graphs of the current device have captured without a workspace."""
     dev = torch.device("cuda", torch.cuda.current_device())
     w = _workspace(dev, _stream(dev), ws)
-    return w.status()
+    rc = w.status()
+    if rc == _c.SSD_OK and ws is None and dev.index in _captured:
+        rc = int(lib.ssd_get_device_status(ctypes.c_void_p(_captured_header()), ctypes.c_void_p(_stream(dev))))
+    return rc
 
 
 def _dims(x, B):

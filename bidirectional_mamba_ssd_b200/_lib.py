@@ -54,6 +54,8 @@ SIGNATURES = {
     "ssd_causal_step": (_i, [_vp] * 7 + [_f] * 2 + [_vp] * 4 + [_ll] * 4 + [_i] * 7 + [_vp, _sz, _vp]),
     "ssd_cache_copy": (_i, [_vp, _ll, _i, _i, _vp, _vp, _i, _vp, _sz, _vp]),
     "ssd_cache_compact": (_i, [_vp, _ll, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "ssd_workspace_init_captured": (_i, [_vp, _sz, _vp]),
+    "ssd_captured_status": (_i, [_vp]),
     "ssd_get_device_status": (_i, [_vp, _vp]),
     "ssd_selftest_wait_timeout": (_i, [_vp, _sz, _i, _vp]),
     "ssd_error_string": (ctypes.c_char_p, [_i]),

@@ -9,8 +9,12 @@ ssd_causal_step, ssd_cache_copy, ssd_cache_compact).
 x, dt, B and C may be views in batch and token (the slices of one projection);
 their last two dimensions (dt: its last) are contiguous.
 
-Calls without a workspace of their own use the stream's, or, while a CUDA graph
-is being captured, one that belongs to the graph: two graphs never share one.
+Calls without a workspace of their own use the stream's. While a CUDA graph is
+being captured they use scratch that belongs to the graph (two graphs never share
+any), and what they report at a replay, on whatever stream, ssd_get_device_status()
+reads from the library's own header of the device. A workspace of the caller's works
+under capture too; it is to have its size before (a call outside the capture gives
+it that), and its own status() has what is reported.
 
 A single token's kernel takes a few microseconds, less than ctypes takes to call it. So
 each function first offers its arguments to csrc/ssd_binding.cpp, which makes the
@@ -22,18 +26,20 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 
 import torch
 
 from . import _binding
-from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _check, _default_ws, _DT, _workspace,
-               lib)
+from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _captured, _captured_header, _check,
+               _default_ws, _DT, _workspace, lib)
 
 _binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                  (lib.ssd_causal_fwd, lib.ssd_causal_step, lib.ssd_cache_copy, lib.ssd_cache_compact)), _default_ws, _check)
 
 _INF = float("inf")
 _INT = 2**31 - 1
+_HEADER = 256          # bytes of a workspace's status header
 _F32, _I32 = torch.float32, torch.int32
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -111,10 +117,39 @@ def _apart(a, b, na, nb):
         raise ValueError(f"{na} and {nb} overlap without being the same array")
 
 
+class _Captured:
+    """The workspace of one call that is being captured: the library's own header where the call needs no more, else memory
+    of the graph's pool, which a node of the graph prepares."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.lock = dev, stream, threading.Lock()
+        _captured.add(dev.index)
+
+    def get(self, nbytes):
+        if nbytes <= _HEADER:
+            return _Header(_captured_header())
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
+        _check(lib.ssd_workspace_init_captured(buf.data_ptr(), nbytes, self.stream), "ssd_workspace_init_captured")
+        return buf
+
+
+class _Header:
+    """The library's own status header, as far as a call looks at a buffer."""
+
+    def __init__(self, address):
+        self.address = address
+
+    def data_ptr(self):
+        return self.address
+
+    def numel(self):
+        return _HEADER
+
+
 def _scratch(dev, stream, workspace):
     """The workspace of a call: the caller's, the graph's being captured, or the stream's."""
     if workspace is None:
-        return Workspace(dev) if _capturing() else _workspace(dev, stream, None)
+        return _Captured(dev, stream) if _capturing() else _workspace(dev, stream, None)
     if workspace.device.index not in (None, dev.index):
         raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
     return workspace

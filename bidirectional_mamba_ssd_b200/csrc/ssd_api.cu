@@ -645,7 +645,8 @@ int ssd_get_device_status(const void *workspace, void *stream) {
     if (cudaStreamSynchronize(s) != cudaSuccess) return SSD_ERR_CUDA;
     if (cudaMemcpy(&st, workspace, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return SSD_ERR_CUDA;
     if (st.flags == 0) return SSD_OK;
-    if (cudaMemset(const_cast<void *>(workspace), 0, sizeof(st)) != cudaSuccess) return SSD_ERR_CUDA;
+    // where else this header reports to stays
+    if (cudaMemset(const_cast<void *>(workspace), 0, offsetof(ssd::DeviceStatus, also)) != cudaSuccess) return SSD_ERR_CUDA;
     if (st.flags & ssd::kFlagTimeout) return SSD_ERR_TIMEOUT;
     return (st.flags & ssd::kFlagIndex) ? SSD_ERR_INDEX : SSD_ERR_CUDA;
 }

@@ -209,7 +209,7 @@ cache_copy_kernel(const CacheArgs a) {
         int s, d;
         bool bad;
         read_pair(a, i, s, d, bad);
-        if (bad && blockIdx.x == 0) atomicOr(&a.status->flags, kFlagIndex);
+        if (bad && blockIdx.x == 0) report(a.status, kFlagIndex);
         if (d >= 0) clash |= (atomicOr(&map[d >> 5], 1u << (d & 31)) >> (d & 31)) & 1u;
     }
     __syncthreads();
@@ -311,7 +311,7 @@ cache_compact_kernel(const CacheArgs a) {
     for (int i = tid; i < a.rows; i += kThreads) {
         const int s = a.table[i];
         if (s >= 0 && s < a.nslots) atomicOr(&map[s >> 5], 1u << (s & 31));
-        else if (s != -1 && blockIdx.x == 0) atomicOr(&a.status->flags, kFlagIndex);
+        else if (s != -1 && blockIdx.x == 0) report(a.status, kFlagIndex);
     }
     __syncthreads();
     // exclusive sums of the words' set bits: a run of words per thread, then the runs

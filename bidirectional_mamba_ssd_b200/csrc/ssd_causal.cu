@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(128) resolve_slots_kernel(const int *slots, in
     bad |= (bool)__syncthreads_or(again);
     if (threadIdx.x == 0) {
         rows[b] = bad ? -1 : s;
-        if (bad) atomicOr(&st->flags, kFlagIndex);
+        if (bad) report(st, kFlagIndex);
     }
 }
 

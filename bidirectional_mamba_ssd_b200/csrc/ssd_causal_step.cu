@@ -73,7 +73,7 @@ causal_step_kernel(const CausalArgs a) {
         if (!skip)
             for (int i = threadIdx.x; i < b; i += 32 * kWarps) again |= a.slots[i] == tag;
         again = __syncthreads_or(again);
-        if ((again || (skip && row != -1)) && threadIdx.x == 0) atomicOr(&a.status->flags, kFlagIndex);
+        if ((again || (skip && row != -1)) && threadIdx.x == 0) report(a.status, kFlagIndex);
         skip |= again;
     }
     T *out = static_cast<T *>(a.out) + ((size_t)b * a.H + h) * a.P;

@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(128) causal_rows_kernel(const CausalArgs a, in
     if (threadIdx.x == 0) {
         rows[b] = row;
         lens[b] = row < 0 ? -1 : a.len(b);
-        if (bad) atomicOr(&a.status->flags, kFlagIndex);
+        if (bad) report(a.status, kFlagIndex);
     }
 }
 

@@ -15,14 +15,22 @@ struct DeviceStatus {
     unsigned int flags;       // kFlag* bits
     unsigned int where;       // id of the wait that expired first (diagnostic)
     unsigned int block;       // blockIdx.x of that wait
-    unsigned int pad[61];
+    unsigned int pad0;
+    DeviceStatus *also;       // a header whose flags are set with these, or nullptr
+    unsigned int pad[58];
 };
 static_assert(sizeof(DeviceStatus) == kStatusBytes, "status header size");
 enum : unsigned int { kFlagTimeout = 1u, kFlagIndex = 2u };
 
+// Sets a flag; returns the flags ahead of it.
+__device__ __forceinline__ unsigned int report(DeviceStatus *st, unsigned int flag) {
+    if (st->also) atomicOr(&st->also->flags, flag);
+    return atomicOr(&st->flags, flag);
+}
+
 __device__ __forceinline__ void report_timeout(DeviceStatus *st, unsigned int where) {
     if (st) {
-        unsigned int old = atomicOr(&st->flags, kFlagTimeout);
+        unsigned int old = report(st, kFlagTimeout);
         if (!(old & kFlagTimeout)) {
             st->where = where;
             st->block = blockIdx.x;

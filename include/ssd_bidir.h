@@ -28,8 +28,8 @@
  *  - All tensor arguments are DEVICE pointers to dense row-major arrays in
  *    natural token order, 16-byte aligned. The caller allocates and owns
  *    every buffer, the workspace included; the library allocates nothing,
- *    keeps no global state and never synchronises (except
- *    ssd_get_device_status).
+ *    keeps no global state (but the header of ssd_captured_status) and never
+ *    synchronises (except ssd_get_device_status).
  *  - "io" = the I/O dtype chosen by `dtype` (SSD_F32 or SSD_BF16): x, dt,
  *    B, C and out use it. A, D and states are always fp32.
  *  - Direction-stacked tensors have a leading dimension of 2:
@@ -123,6 +123,18 @@ size_t ssd_workspace_bytes(int op, int batch, int seqlen, int nheads, int headdi
 /* Zero the workspace's status header (256 bytes) on `stream`. A workspace
  * must be initialised once before first use (zero-filled memory counts). */
 int ssd_workspace_init(void *workspace, size_t ws_bytes, void *stream);
+
+/* Calls captured into a CUDA graph. A workspace that belongs to the graph has
+ * nobody to read its header after a replay. ssd_workspace_init_captured is
+ * ssd_workspace_init for such a workspace: from then on (captured with the
+ * calls: at every replay) what calls report in its header, they report in the
+ * library's own as well, one per device. ssd_captured_status gives that header's
+ * address on the current device: pass it to ssd_get_device_status, and as the
+ * workspace (256 bytes) of calls that need no more than the header; any number
+ * of graphs and streams may share it for that. The first of either call on a
+ * device loads 256 bytes of device memory; both may be made during a capture. */
+int ssd_workspace_init_captured(void *workspace, size_t ws_bytes, void *stream);
+int ssd_captured_status(void **header);
 
 /* Full-sequence bidirectional mixer (both scans over the whole sequence).
  *   x    (batch, seqlen, nheads, headdim)           io

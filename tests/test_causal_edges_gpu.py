@@ -2,6 +2,9 @@
 given, against the recurrence in 64 bits (causal_ref), at the tolerances of
 test_causal_gpu where a test derives none of its own."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -154,3 +157,91 @@ def test_pools_of_two_sizes_at_once(ssd, width):
     [t.start() for t in ts]
     [t.join() for t in ts]
     assert not refused, (len(refused), refused[:3])
+
+
+def _captured_calls(ssd):
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    t = inputs((2,), 2, 64, 64, 1, "bf16", seed=51)
+    d = inputs((2, 300), 2, 64, 64, 1, "bf16", seed=52)
+    w = inputs((2500,), 1, 64, 64, 1, "bf16", seed=53)
+    pool, wide = torch.zeros(4, 2, 64, 64, device="cuda"), torch.zeros(2600, 1, 64, 64, device="cuda")
+    slots, many = i32(1, 0), torch.arange(2500, dtype=torch.int32, device="cuda")
+    pages, to = i32(1, 0), i32(3, 2)
+    f = ssd.ssd_causal_fwd
+    return {
+        "step": (slots, lambda: ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], t["D"], pool, slots)),
+        "many": (many, lambda: ssd.ssd_causal_step(w["x"], w["dt"], w["A"], w["B"], w["C"], w["D"], wide, many)),
+        "copy": (pages, lambda: ssd.ssd_cache_copy(pool[None], pages, to)),
+        "compact": (pages, lambda: ssd.ssd_cache_compact(pool[None], pages)),
+        "prompt": (slots, lambda: f(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], pool, slots=slots)),
+        "scan": (slots, lambda: f(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], pool, slots=slots, path=ssd.SSD_PATH_SIMT)),
+    }
+
+
+@pytest.mark.parametrize("name", ["step", "many", "copy", "compact", "prompt", "scan"])
+def test_bad_index_in_a_replay_is_reported(ssd, name):
+    """Captured without a workspace: an index that is bad at a replay is reported by ssd_get_device_status, once, on
+    whatever stream the graph runs; an index that is good again is not."""
+    idx, call = _captured_calls(ssd)[name]
+    good = idx.clone()
+    call()                                    # loads the kernels
+    torch.cuda.synchronize()
+    assert ssd.ssd_get_device_status() == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            g.replay()
+            assert ssd.ssd_get_device_status() == 0
+            idx[1] = 100000
+            g.replay()
+            idx.copy_(good)
+            g.replay()
+            assert ssd.ssd_get_device_status() == ssd.SSD_ERR_INDEX
+            assert ssd.ssd_get_device_status() == 0
+            stream.synchronize()
+
+
+def test_captured_calls_add_no_fill(ssd):
+    """A captured single token, copy and compaction are one node each."""
+    cudart = ctypes.CDLL("libcudart.so.12")
+    for name in ("step", "copy", "compact"):
+        _, call = _captured_calls(ssd)[name]
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(g):
+            call()
+        n = ctypes.c_size_t()
+        assert cudart.cudaGraphGetNodes(ctypes.c_void_p(g.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+        assert n.value == 1, f"{name}: {n.value} nodes"
+
+
+FIRST = """
+import sys
+sys.path.insert(0, %r)
+import torch
+import bidirectional_mamba_ssd_b200 as ssd
+x, dt, bc = (torch.ones(2, *s, device="cuda") for s in ((2, 64), (2,), (1, 64)))
+A, pool = -torch.ones(2, device="cuda"), torch.zeros(4, 2, 64, 64, device="cuda")
+slots = torch.tensor([1, 9], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = ssd.ssd_causal_step(x, dt, A, bc, bc, None, pool, slots)
+    z, _ = ssd.ssd_causal_fwd(x[:, None], dt[:, None], A, bc[:, None], bc[:, None], None, pool, slots=slots)
+assert ssd.ssd_get_device_status() == 0
+g.replay()
+assert ssd.ssd_get_device_status() == ssd.SSD_ERR_INDEX
+# h = 1, then exp(-1) + 1; 64 of them a sum
+want = torch.tensor([64.0, 64 * (1 + torch.exp(torch.tensor(-1.0)).item())])
+assert torch.allclose(torch.stack([y[0, 0, 0], z[0, 0, 0, 0]]).cpu(), want, rtol=1e-5), (y[0, 0, 0], z[0, 0, 0, 0])
+assert (y[1] == 0).all() and (z[1] == 0).all()
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing has been called before the capture: neither the kernels nor the library's own header are loaded yet."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST % root], capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr[-2000:]
