@@ -111,7 +111,12 @@ class Workspace:
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            # what calls have reported and status() has not read yet stays (a copy that a graph
+            # captures would report it again at every replay)
+            if self.buf is not None and not (buf.is_cuda and torch.cuda.is_current_stream_capturing()):
+                buf[:256].copy_(self.buf[:256])
+            self.buf = buf
         return self.buf
 
     def status(self) -> int:

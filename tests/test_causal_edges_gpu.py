@@ -245,3 +245,17 @@ def test_first_calls_of_a_process_are_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", FIRST % root], capture_output=True, text=True, timeout=120)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_status_outlives_a_larger_workspace(ssd):
+    """A bad slot is reported although a later call on the same stream has made the workspace grow since."""
+    t = inputs((2,), 2, 64, 64, 1, "bf16", seed=54)
+    d = inputs((2, 300), 2, 64, 64, 1, "bf16", seed=55)
+    pool = torch.zeros(4, 2, 64, 64, device="cuda")
+    slots = torch.tensor([1, 9], dtype=torch.int32, device="cuda")
+    for ws in (ssd.Workspace(), None):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ssd.ssd_causal_step(t["x"], t["dt"], t["A"], t["B"], t["C"], t["D"], pool, slots, workspace=ws)
+            ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], workspace=ws)
+            assert ssd.ssd_get_device_status(ws) == ssd.SSD_ERR_INDEX
+            assert ssd.ssd_get_device_status(ws) == 0

@@ -54,3 +54,12 @@ def test_every_call_holds_its_workspace(monkeypatch, name):
     calls(ws)[name]()
     assert made and all(held for _, held in made), made
     assert not ws.lock.locked()
+
+
+def test_a_larger_buffer_keeps_the_status_header():
+    ws = ssd.Workspace("cpu")
+    ws.get(300)[:256] = torch.arange(256, dtype=torch.uint8)
+    ws.buf[256:] = 9
+    buf = ws.get(1000)
+    assert buf.numel() == 1000 and buf[:256].tolist() == list(range(256)) and not buf[256:].any()
+    assert ws.get(500) is buf
