@@ -8,7 +8,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssd_bidir.so")
 
 # Values of include/ssd_bidir.h.
@@ -68,11 +67,9 @@ _lib = None
 def load():
     global _lib
     if _lib is None:
-        for path in (LIB_PATH, BINDING_PATH):
-            if os.path.exists(path):
-                continue
+        if not os.path.exists(LIB_PATH):
             raise ImportError(
-                f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
+                f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
                 "(nvcc, sm_100a). There is no fallback implementation.")
         lib = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in SIGNATURES.items():

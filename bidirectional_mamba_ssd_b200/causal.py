@@ -20,22 +20,42 @@ A single token's kernel takes a few microseconds, less than ctypes takes to call
 each function first offers its arguments to csrc/ssd_binding.cpp, which makes the
 call if all of them are as they should be; what follows here is for the calls that it
 leaves alone: bad arguments (their messages), another device than the current one,
-a workspace that has yet to be made or to grow, and a graph's own under capture.
+a workspace that has yet to be made or to grow, and a graph's own under capture. Where
+that extension is missing or built for another torch, every call takes this way.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import threading
+import warnings
 
 import torch
 
-from . import _binding
 from . import (SSD_OP_CAUSAL_FWD, SSD_OP_CAUSAL_STEP, SSD_PATH_AUTO, Workspace, _captured, _captured_header, _check,
                _default_ws, _DT, _workspace, lib)
 
-_binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                 (lib.ssd_causal_fwd, lib.ssd_causal_step, lib.ssd_cache_copy, lib.ssd_cache_compact)), _default_ws, _check)
+
+class _Absent:
+    """In the extension's place where it is missing or unfit: leaves every call to this module."""
+    causal_fwd = causal_step = cache_copy = cache_compact = staticmethod(lambda *a: NotImplemented)
+
+
+def _load_binding():
+    try:
+        from . import _binding as b
+        if b.torch_version != str(torch.__version__):
+            raise ImportError(f"built for torch {b.torch_version}, this is {torch.__version__}")
+        entries = (lib.ssd_causal_fwd, lib.ssd_causal_step, lib.ssd_cache_copy, lib.ssd_cache_compact)
+        b.setup(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), _default_ws, _check)
+        return b
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"the C++ part of the serving calls' binding is not used, calls take longer on the host ({e}); "
+                      "it is built by `python -c 'import __graft_entry__ as g; g.build()'`", RuntimeWarning, stacklevel=2)
+        return _Absent
+
+
+_binding = _load_binding()
 
 _INF = float("inf")
 _INT = 2**31 - 1

@@ -154,11 +154,21 @@ class Scratch {
   private:
     void release() {
         if (held_) {
-            PyObject *error = PyErr_GetRaisedException();    // a refused call's, kept across this one
+            // a refused call's error is kept across this one
+#if PY_VERSION_HEX >= 0x030C0000
+            PyObject *error = PyErr_GetRaisedException();
+#else
+            PyObject *type, *value, *trace;
+            PyErr_Fetch(&type, &value, &trace);
+#endif
             PyObject *got = PyObject_CallMethodNoArgs(lock_, s_release);
             if (!got) PyErr_Clear();
             Py_XDECREF(got);
+#if PY_VERSION_HEX >= 0x030C0000
             PyErr_SetRaisedException(error);
+#else
+            PyErr_Restore(type, value, trace);
+#endif
             held_ = false;
         }
         Py_CLEAR(lock_);
@@ -418,5 +428,8 @@ PyMODINIT_FUNC PyInit__binding() {
     s_acquire = PyUnicode_InternFromString("acquire");
     s_release = PyUnicode_InternFromString("release");
     if (!s_buf || !s_lock || !s_acquire || !s_release) return nullptr;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // torch's classes are used as this version lays them out: causal.py compares
+    if (m && PyModule_AddStringConstant(m, "torch_version", SSD_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
 }
