@@ -119,6 +119,18 @@ class Workspace:
             self.buf = buf
         return self.buf
 
+    # stored, and copied with its buffer, without the lock
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "lock"}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state, lock=threading.Lock())
+
+    def __copy__(self):           # a shallow copy has the same buffer, and so the same lock
+        twin = object.__new__(type(self))
+        twin.__dict__.update(self.__dict__)
+        return twin
+
     def status(self) -> int:
         """Synchronise the current stream and read (and clear) the status header."""
         if self.buf is None:

@@ -1,5 +1,8 @@
 """Host-only checks of the Workspace class and of who holds its lock (nothing is
 launched: the library's calls are replaced by recorders)."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -63,3 +66,17 @@ def test_a_larger_buffer_keeps_the_status_header():
     buf = ws.get(1000)
     assert buf.numel() == 1000 and buf[:256].tolist() == list(range(256)) and not buf[256:].any()
     assert ws.get(500) is buf
+
+
+def test_copies_and_stored_workspaces():
+    """A workspace, and an object that holds one, can be copied and stored; a copy has a buffer and a lock of its own."""
+    ws = ssd.Workspace("cpu")
+    ws.get(300)[0] = 7
+    with ws.lock:
+        twins = [copy.deepcopy(ws), pickle.loads(pickle.dumps(ws)), copy.deepcopy({"cache": [ws]})["cache"][0]]
+    for w in twins:
+        assert w.device == ws.device and w.buf[0] == 7 and w.buf.data_ptr() != ws.buf.data_ptr()
+        assert w.lock is not ws.lock and not w.lock.locked()
+        assert w.get(400).numel() == 400
+    same = copy.copy(ws)
+    assert same.buf is ws.buf and same.lock is ws.lock
