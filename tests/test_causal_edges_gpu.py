@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import causal_ref as ref
-from test_causal_gpu import check_out, check_state, inputs, paths_of, sizes
+from test_causal_gpu import check_out, check_state, inputs, opts, paths_of, sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -99,6 +99,65 @@ def test_nan_in_a_raw_step_size_shows(ssd, io, hi):
     torch.cuda.synchronize()
     assert torch.isnan(y[1, 1]).all() and torch.isnan(st[1, 1]).all()
     assert torch.isfinite(y[0]).all() and torch.isfinite(st[0]).all() and torch.isfinite(y[1, [0, 2]]).all()
+
+
+# lengths, H, P, N, G: 148 units or more, so that units are cut between neighbouring CTAs
+CUT = [([2500, 0, 300, 1, 129, 128, 0, 257, 700, 64, 5, 127, 130, 256, 999, 1500], 10, 64, 128, 1),
+       ([1, 7, 3000, 2, 100, 0, 384, 385, 50, 640], 8, 128, 64, 2),
+       ([400] * 25, 6, 64, 128, 3)]
+
+
+@pytest.mark.parametrize("case", CUT, ids=["one_long", "two_halves", "even"])
+def test_units_cut_over_several_ctas(ssd, case):
+    """Ragged prompts into a pool in place, with padding, bad and repeated slots, of so many units that the tiles of a unit
+    are shared by neighbouring CTAs, by three and more of them where one prompt is long; the same again, bit by bit."""
+    lens, H, P, N, G = case
+    batch, L = len(lens), max(lens)
+    nslots = batch + 4
+    d = inputs((batch, L), H, P, N, G, "bf16", seed=43 + batch, raw=True, packed=True)
+    pool = torch.randn(nslots, H, P, N, generator=d["g"], device="cuda") * 0.3
+    slots = torch.randperm(nslots, generator=d["g"], device="cuda")[:batch].to(torch.int32)
+    slots[3], slots[4], slots[5] = -1, nslots, slots[0]
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    good = [b for b in range(batch) if b not in (3, 4, 5)]
+    behind = torch.arange(L, device="cuda")[None, :] >= seqlens[:, None]
+    o, oh = ref.fwd(d["x"][good], sizes(d)[good], d["A"], d["B"][good], d["C"][good], d["D"], pool[slots[good].long()],
+                    [lens[b] for b in good])
+    for k in ("x", "dt", "B", "C"):
+        d[k][behind] = float("nan")
+    got = []
+    for _ in range(3):
+        st, out = pool.clone(), torch.full((batch, L, H, P), 7.0, dtype=torch.bfloat16, device="cuda")
+        y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], st, seqlens=seqlens, slots=slots, out=out,
+                                  **opts(d))
+        torch.cuda.synchronize()
+        assert ssd.ssd_get_device_status() == ssd.SSD_ERR_INDEX and y is out and h is st
+        got.append((y, h))
+    assert all(torch.equal(a, b) for pair in got[1:] for a, b in zip(pair, got[0]))
+    assert (y[behind] == 0).all() and (y[[3, 4, 5]] == 0).all()
+    for k, b in enumerate(good):
+        if lens[b]:
+            check_out(y[b, :lens[b]], o[k, :lens[b]], "bf16", f"row {b}")
+        check_state(h[slots[b]], oh[k], f"row {b}")
+    rest = sorted(set(range(nslots)) - set(slots[good].tolist()))
+    assert torch.equal(h[rest], pool[rest])
+
+
+def test_fp32_scan_decays_around_its_border(ssd):
+    """The CUDA-core scan rescales the state once for four tokens that decay by at most e^-8: step sizes of 0.1 with decays
+    of e^-7.8 and e^-8.2 a four, and a head that changes within the sequence, at lengths that end inside a four."""
+    A = torch.tensor([-19.5, -20.5, -1.0], device="cuda")
+    for L in (1, 3, 6, 33, 203, 700):
+        d = inputs((1, L), 3, 64, 64, 1, "f32", seed=60 + L)
+        d["dt"][:, :, :2] = 0.1
+        d["dt"][:, ::7, 2] = 30.0
+        h0 = torch.randn(1, 3, 64, 64, generator=d["g"], device="cuda")
+        o, oh = ref.fwd(d["x"], sizes(d), A, d["B"], d["C"], d["D"], h0, [L])
+        y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], A, d["B"], d["C"], d["D"], h0)
+        torch.cuda.synchronize()
+        for k in range(3):
+            check_out(y[:, :, k], o[:, :, k], "f32", f"L {L} head {k}")
+            check_state(h[:, k], oh[:, k], f"L {L} head {k}")
 
 
 @pytest.mark.parametrize("io,path", [("f32", "SIMT"), ("bf16", "SIMT"), ("bf16", "AUTO")])
