@@ -185,7 +185,10 @@ def ssd_causal_fwd(x, dt, A, B, C, D=None, init=None, *, seqlens=None, slots=Non
     init: start states, (batch, H, P, N), or with slots (batch) int32 a pool
     (nslots, H, P, N) whose page slots[b] is row b's; None starts from zero.
     state_out: where the end states go, laid out as init; with slots it
-    defaults to init (in place). dt_bias (H): dt is the raw projection."""
+    defaults to init (in place). dt_bias (H): dt is the raw projection.
+    path: SSD_PATH_AUTO takes bf16 inputs to the tensor cores, which round the
+    masked C.B^T tile and the copy of the state that outputs read to bf16 (end
+    states keep fp32 accuracy); SSD_PATH_SIMT rounds nothing but the output."""
     got = _binding.causal_fwd(x, dt, A, B, C, D, init, seqlens, slots, dt_bias, dt_min, dt_max, out, state_out, path,
                               workspace)
     if got is not NotImplemented:

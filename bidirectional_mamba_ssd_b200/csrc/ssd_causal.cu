@@ -15,8 +15,9 @@
 // e^-8 they go one by one, by the same code with the others' terms left out. Tokens arrive
 // in chunks of kTok through cp.async, two chunks deep.
 // What bounds it: with many units instruction issue and shared memory together (fp32, 64
-// x 500 tokens, 24 heads of 64, N = 128: 480 us; token by token with a butterfly each 543,
-// with a rescaling each as well 581; 64 columns a CTA 557, 16 517), with few a warp's own
+// sequences of even lengths up to 500 tokens, 24 heads of 64, N = 128: 477 us; token by token
+// with a butterfly each 543, with a rescaling each as well 581; 64 columns a CTA 557, 16 517; 64
+// full sequences 837, and 2877 where four tokens decay by more than e^-8), with few a warp's own
 // time per token; there the sequence is cut into segments (own end states, a carry, then
 // the outputs), which costs a second pass over x and B.
 #include <stdint.h>
@@ -327,9 +328,9 @@ __global__ void __launch_bounds__(256) causal_carry_kernel(const CausalArgs a, c
     }
 }
 
-// Columns of a CTA: 128 threads. fp32, 32 and 64 columns: 4 x 777 tokens, 8 heads of
-// 128, N = 64 49.5 and 46.9 us, 100 x 300 tokens 184 and 175; N = 128, 64 x 500 tokens, 24
-// heads of 64 479 and 557. (With the registers that a kernel without a bound on its CTAs
+// Columns of a CTA: 128 threads. fp32, even lengths up to the one given, 32 and 64 columns: 4 x
+// 777 tokens, 8 heads of 128, N = 64 49.5 and 46.6 us, 100 x 300 tokens 184 and 176; N = 128, 64 x
+// 500 tokens, 24 heads of 64 477 and 557. (With the registers that a kernel without a bound on its CTAs
 // gets, 32 columns of N = 128 and 64 of N = 64 take 483, 50.2 and 165.)
 constexpr int cols_of(int N) { return 4096 / N; }
 
