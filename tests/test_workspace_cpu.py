@@ -6,12 +6,18 @@ import pickle
 import pytest
 import torch
 
-import bidirectional_mamba_ssd_b200 as ssd
-
 B, L, H, P, N, G = 2, 8, 2, 64, 64, 1
 
 
-def calls(ws):
+@pytest.fixture(scope="module")
+def ssd():
+    import __graft_entry__
+    __graft_entry__.build()
+    import bidirectional_mamba_ssd_b200 as m
+    return m
+
+
+def calls(ssd, ws):
     """Every entry point that takes a workspace and is called over ctypes, with small CPU tensors."""
     io = torch.bfloat16
     z = lambda *s: torch.zeros(*s, dtype=io)  # noqa: E731
@@ -35,8 +41,8 @@ def calls(ws):
     }
 
 
-@pytest.mark.parametrize("name", sorted(calls(None)))
-def test_every_call_holds_its_workspace(monkeypatch, name):
+@pytest.mark.parametrize("name", sorted(calls(None, None)))
+def test_every_call_holds_its_workspace(ssd, monkeypatch, name):
     """A call's launches share the workspace's buffer: its lock is held from the buffer's choice to the last launch, so that
     no other thread's call on the same stream comes between them."""
     ws = ssd.Workspace("cpu")
@@ -54,12 +60,12 @@ def test_every_call_holds_its_workspace(monkeypatch, name):
     monkeypatch.setattr(ssd, "lib", Lib())
     monkeypatch.setattr(ssd, "_need", lambda *a, **k: None)
     monkeypatch.setattr(ssd, "_stream", lambda device: 0)
-    calls(ws)[name]()
+    calls(ssd, ws)[name]()
     assert made and all(held for _, held in made), made
     assert not ws.lock.locked()
 
 
-def test_a_larger_buffer_keeps_the_status_header():
+def test_a_larger_buffer_keeps_the_status_header(ssd):
     ws = ssd.Workspace("cpu")
     ws.get(300)[:256] = torch.arange(256, dtype=torch.uint8)
     ws.buf[256:] = 9
@@ -68,7 +74,7 @@ def test_a_larger_buffer_keeps_the_status_header():
     assert ws.get(500) is buf
 
 
-def test_copies_and_stored_workspaces():
+def test_copies_and_stored_workspaces(ssd):
     """A workspace, and an object that holds one, can be copied and stored; a copy has a buffer and a lock of its own."""
     ws = ssd.Workspace("cpu")
     ws.get(300)[0] = 7
