@@ -26,17 +26,20 @@
 // 320: 132, 131, 143, 155 us (one factor, two, an exponential an entry for the last two).
 //
 // Roundings to bf16: M and the copy of H that enters C H, both operands of
-// products whose result is rounded to bf16 (relative 2^-9 a term, random). The
-// state is a result in fp32, so diag(w) X enters S as three bf16 terms (24 bits),
-// and H stays in fp32 registers.
+// products whose result is rounded to bf16 (relative 2^-9 a term, random). A token's
+// own term G_tt dt_t x_t is kept out of M and joins D x in fp32: with few terms in a row
+// (short prompts, strong decay) it may be as large as D x and of the other sign, and its
+// rounding then stood at up to 1.6 % of the outputs (130M shape 158 to 160 us for it, 16 x
+// 1000 ragged 60.2 to 60.7). The state is a result in fp32, so diag(w) X enters S as
+// three bf16 terms (24 bits), and H stays in fp32 registers.
 //
 // What bounds it: on paper HBM (x, B, C and y once); as measured the work of a tile
 // within an SM. 32 x 1024 tokens, 24 heads of 64, N = 128 (631 MB, 96 us at the rate of
-// a copy): 132 us in a short run at 1.96 GHz, 157 us in a long one, where the
+// a copy): 132 us in a short run at 1.96 GHz, 160 us in a long one, where the
 // power limit holds the clock near 1.55 GHz. A tile takes an SM about 5500 cycles:
 // nearly 3000 of shared-memory traffic (the MMAs' operands and the terms of diag(w) X),
 // around which mask, state and output have to fit. One sequence of 65536 tokens (1.21
-// GB, 185 us): 436 us, of which the pass for the states takes a third.
+// GB, 185 us): 437 us, of which the pass for the states takes a third.
 //
 // Work is cut so that every CTA has
 // the same number of tiles: the tiles of all units in order, divided evenly. A
@@ -408,6 +411,16 @@ __device__ __forceinline__ void split3(uint4 x, float w, uint4 (&t)[3]) {
             if (k < 2) a = fma2(pair_of(lo & 0xffff0000u, hi & 0xffff0000u), minus, a);
         }
     }
+}
+// v[i] of registers, by halves
+__device__ __forceinline__ uint32_t pick(const uint32_t (&v)[16], int i) {
+    uint32_t a[8], b[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = i & 8 ? v[k + 8] : v[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[k] = i & 4 ? a[k + 4] : a[k];
+    const uint32_t c = i & 2 ? b[2] : b[0], d = i & 2 ? b[3] : b[1];
+    return i & 1 ? d : c;
 }
 __device__ __forceinline__ void sync_state() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -909,12 +922,24 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tc_fence_after();
             const uint32_t tg = tG(n) + lane_off;
             const int chunks = 2 * wq + 2;             // up to and with the diagonal
-            // entries behind the row's own token are dropped, never multiplied
+            // the row's own G, for the output (two loads of its own: taken out of the chunks as the
+            // mask passes them the 130M shape takes 161 to 163 us, out of the last two kept 166)
+            float g_own;
+            {
+                uint32_t lo[16], hi[16];
+                tmem_ld16(tg + 32 * wq, lo);
+                tmem_ld16(tg + 32 * wq + 16, hi);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 16; ++q) lo[q] = lane & 16 ? hi[q] : lo[q];
+                g_own = __uint_as_float(pick(lo, lane & 15));
+            }
+            // the row's own entry and those behind it are dropped, never multiplied
             auto put = [&](int c, uint32_t (&m)[8]) {
                 if (c >= 2 * wq) {
                     const int own = row - 16 * c;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) m[q] = 2 * q + 1 <= own ? m[q] : 2 * q <= own ? (m[q] & 0xffffu) : 0u;
+                    for (int q = 0; q < 8; ++q) m[q] = 2 * q + 1 < own ? m[q] : 2 * q < own ? (m[q] & 0xffffu) : 0u;
                 }
                 tmem_st8(tg + 8 * c, m);
             };
@@ -968,7 +993,8 @@ causal_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // ---------------- the output
             const int t = I.t0 + row;
             const bool own = !one && !(I.flags & kZeroStart);       // C H comes by itself, with the row's decay
-            const float rf = factor ? __expf(my_a - I.ref[wq >> 1]) : 1.f, e = __expf(my_a), D = I.D;
+            const float rf = factor ? __expf(my_a - I.ref[wq >> 1]) : 1.f, e = __expf(my_a);
+            const float D = I.D + rf * (g_own * col[row]);       // of the row's own x
             __nv_bfloat16 *dst = p.out + (((size_t)I.b * p.L + t) * p.HU + I.hu) * 64;
             const bool keep = t < I.len, inside = t < p.L, partial = I.flags & kPartial;
             const pair_t rf2 = pair_of(rf, rf), D2 = pair_of(D, D);

@@ -447,8 +447,8 @@ int ssd_bidir_bwd_seeded(const void *x, const void *dt, const float *A, const vo
  * path: SSD_PATH_AUTO, SSD_PATH_SIMT (the CUDA-core scan, either dtype) or
  * SSD_PATH_FUSED (the tensor-core kernel, bf16; what AUTO takes for bf16). With
  * bf16 the state is carried and returned in fp32 with fp32 accuracy on either
- * path; on the tensor cores the masked C.B^T tile and the copy of the state
- * that the outputs read are rounded to bf16, and each term of an output
+ * path; on the tensor cores the masked C.B^T tile (but for its diagonal) and
+ * the copy of the state that the outputs read are rounded to bf16, and each term of an output
  * (dt (C.B) x of an earlier token, C h) is to lie below 1e20 in magnitude; terms
  * below 1e-20 may lose accuracy. SSD_PATH_SIMT rounds nothing to bf16 but the
  * output and has fp32's own range. Workspace:

@@ -77,6 +77,35 @@ def test_fwd_decays_at_any_magnitude(ssd, scale):
         check_state(h[:, k], oh[:, k], f"decay {s}")
 
 
+@pytest.mark.parametrize("L", [1, 130])
+def test_a_tokens_own_term_against_the_skip_term(ssd, L):
+    """A token's own C.B dt x and its skip term may nearly cancel (single tokens, or decays that leave nothing else): both are
+    kept in fp32. A sum G of 128 products in fp32 is off by at most 128 x 2^-24 of their magnitudes F, the two exponentials
+    that make 1 by 2^-20 (2^-21 each), so
+        |y - o| <= (2^-17 F + 2^-20 |G|) dt |x| + 2^-23 (|G| dt + |D|) |x| + half a step of the output."""
+    B_, H, P, N = 3, 4, 64, 128
+    d = inputs((B_, L), H, P, N, H, "bf16", seed=80 + L)
+    d["dt"].fill_(0.1)
+    d["B"], d["C"] = d["B"][:1, :1].repeat(B_, L, 1, 1), d["C"][:1, :1].repeat(B_, L, 1, 1)     # one G a head
+    # L = 1: masks of one factor (decays of e^-0.1, e^-10, e^-70) and of exponentials (e^-120); L = 130: of exponentials, and
+    # e^-50 or less is left of a token at the next
+    A = -torch.tensor([5e2, 6e2, 1e3, 1e4], device="cuda") if L > 1 else -torch.tensor([1.0, 100.0, 700.0, 1200.0], device="cuda")
+    dt = d["dt"].double().cpu()[0, 0]
+    Bd, Cd, x = (d[k].double().cpu() for k in ("B", "C", "x"))
+    G, F = (Bd[0, 0] * Cd[0, 0]).sum(-1), (Bd[0, 0] * Cd[0, 0]).abs().sum(-1)
+    D = (-(G * dt) * (1 - 2 ** -6)).float().cuda()
+    o, oh = ref.fwd(d["x"], d["dt"].double().cpu(), A, d["B"], d["C"], D, torch.zeros(B_, H, P, N), [L] * B_)
+    y, h = ssd.ssd_causal_fwd(d["x"], d["dt"], A, d["B"], d["C"], D)
+    torch.cuda.synchronize()
+    y = y.double().cpu()
+    unit = ((2 ** -17 * F + 2 ** -20 * G.abs()) * dt + 2 ** -23 * (G.abs() * dt + D.double().cpu().abs()))[:, None] * x.abs()
+    top = torch.maximum(y.abs(), o.abs()).clamp(min=2.0 ** -126)
+    off = (y - o).abs() / (unit + 0.5 * torch.exp2(torch.floor(torch.log2(top)) - 7))
+    for k in range(H):
+        assert off[:, :, k].max() <= 1, f"head {k}: {off[:, :, k].max():.2f} of the bound"
+    check_state(h, oh, "states")
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("hi", [0.1, float("inf")])
 def test_nan_in_a_raw_step_size_shows(ssd, io, hi):
